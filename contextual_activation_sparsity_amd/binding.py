@@ -35,6 +35,7 @@ SFN_PIPE_SEQUENTIAL, SFN_PIPE_PARALLEL = 0, 1
 SFN_WORKSPACE_HEADER_BYTES, SFN_WORKSPACE_STATUS_OFFSET = 2048, 1024
 SFN_STATUS_BALANCER_TIMEOUT, SFN_STATUS_PREDICTOR_TIMEOUT = 1, 2
 SFN_NOALLOC_SCRATCH_BYTES = 32 << 20
+SFN_MAX_REQUESTS, SFN_MAX_STEP_TOKENS, SFN_MAX_HEADS = 4096, 262144, 1024
 
 EXPORTED = (
     "sparse_ffn_workspace_size",
@@ -48,6 +49,11 @@ EXPORTED = (
     "sparse_ffn_decode_svd",
     "svd_predict",
     "ffn_dense_chunk",
+    "kv_cache_plan",
+    "kv_cache_append",
+    "kv_cache_attend_workspace_size",
+    "kv_cache_attend",
+    "residual_norm",
 )
 
 
@@ -63,6 +69,20 @@ class sfn_svd(ctypes.Structure):
     _fields_ = [
         ("d", ctypes.c_int32), ("f", ctypes.c_int32), ("r", ctypes.c_int32), ("reserved", ctypes.c_int32),
         ("q", ctypes.c_void_p), ("l", ctypes.c_void_p), ("b", ctypes.c_void_p), ("tau", ctypes.c_void_p),
+    ]
+
+
+class sfn_kv(ctypes.Structure):
+    _fields_ = [
+        ("n_pages", ctypes.c_int32), ("page", ctypes.c_int32), ("h_kv", ctypes.c_int32), ("dh", ctypes.c_int32),
+        ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+    ]
+
+
+class sfn_norm(ctypes.Structure):
+    _fields_ = [
+        ("d", ctypes.c_int32), ("wdtype", ctypes.c_int32), ("eps", ctypes.c_float), ("scale", ctypes.c_float),
+        ("w_post", ctypes.c_void_p), ("w_pre", ctypes.c_void_p),
     ]
 
 
@@ -90,6 +110,19 @@ _lib.svd_predict.argtypes = [ctypes.POINTER(sfn_svd), _vp, _vp, _vp, _vp, _vp, _
 _lib.svd_predict.restype = ctypes.c_int
 _lib.ffn_dense_chunk.argtypes = [ctypes.POINTER(sfn_ffn), _vp, _i32, _vp, _vp, _sz, _vp]
 _lib.ffn_dense_chunk.restype = ctypes.c_int
+_i64 = ctypes.c_int64
+_lib.kv_cache_plan.argtypes = [ctypes.POINTER(sfn_kv), _i32, _i32, _i32] + [_vp] * 13
+_lib.kv_cache_plan.restype = ctypes.c_int
+_lib.kv_cache_append.argtypes = [ctypes.POINTER(sfn_kv), _i32, _i32, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i32,
+                                 _i32, _vp, _vp]
+_lib.kv_cache_append.restype = ctypes.c_int
+_lib.kv_cache_attend_workspace_size.argtypes = [ctypes.POINTER(sfn_kv), _i32, _i32, _i32, _i32, _i32]
+_lib.kv_cache_attend_workspace_size.restype = _sz
+_lib.kv_cache_attend.argtypes = [ctypes.POINTER(sfn_kv), _i32, _i32, _i32, _vp, _i64, _vp, _i32, _vp, _vp, _i32, _i32, _f32,
+                                 _i32, _vp, _vp, _sz, _vp]
+_lib.kv_cache_attend.restype = ctypes.c_int
+_lib.residual_norm.argtypes = [ctypes.POINTER(sfn_norm), _i32, _vp, _i32, _vp, _i32, _vp, _i64, _vp, _vp, _vp]
+_lib.residual_norm.restype = ctypes.c_int
 
 
 class SparseFFNError(RuntimeError):
@@ -282,6 +315,129 @@ def ffn_dense_chunk(layer: FFNLayer, x: torch.Tensor, y: torch.Tensor, ws: torch
         _ptr(y, "y", torch.float32, n * layer.d), _ptr(ws, "ws"), ws.numel() * ws.element_size(),
         _stream(stream))
     _check(st, "ffn_dense_chunk")
+
+
+@dataclass
+class KVCache:
+    """One layer's paged key/value cache: k and v [n_pages, h_kv, page, dh], bfloat16 or
+    float32, page 16, 32, 64, 128 or 256 tokens, dh 64 or 128."""
+
+    k: torch.Tensor
+    v: torch.Tensor
+
+    def __post_init__(self):
+        if self.k.dim() != 4 or self.k.shape != self.v.shape or self.k.dtype != self.v.dtype:
+            raise ValueError("k and v must both be [n_pages, h_kv, page, dh] of one dtype")
+        if self.k.dtype not in _WDT:
+            raise ValueError("the cache must be bfloat16 or float32")
+        self.n_pages, self.h_kv, self.page, self.dh = self.k.shape
+        self.dtype = self.k.dtype
+        self.c = sfn_kv(self.n_pages, self.page, self.h_kv, self.dh, _WDT[self.dtype], 0, _ptr(self.k, "k"),
+                        _ptr(self.v, "v"))
+
+
+@dataclass
+class ResidualNorm:
+    """Weights of residual_norm, [d] each: w_pre of the norm before the next block, w_post
+    (optional) of the norm after the last one, the residual scale and the norms' eps."""
+
+    w_pre: torch.Tensor
+    w_post: Optional[torch.Tensor] = None
+    eps: float = 1e-5
+    scale: float = 1.0
+
+    def __post_init__(self):
+        if self.w_pre.dtype not in _WDT:
+            raise ValueError("weights must be bfloat16 or float32")
+        self.d, self.dtype = self.w_pre.numel(), self.w_pre.dtype
+        if self.w_post is not None and self.w_post.numel() != self.d:
+            raise ValueError(f"w_post must be [{self.d}]")
+        self.c = sfn_norm(self.d, _WDT[self.dtype], float(self.eps), float(self.scale),
+                          _ptr(self.w_post, "w_post", self.dtype), _ptr(self.w_pre, "w_pre"))
+
+
+def _token_rows(t: torch.Tensor, name, dtype, heads, dh):
+    """Address and token stride (elements) of [T, heads, dh] rows, or of parts of wider rows."""
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be a GPU tensor (got {t.device})")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype} (got {t.dtype})")
+    n, h, w = t.shape
+    s0, s1, s2 = t.stride()
+    if w != dh or (heads is not None and h != heads):
+        raise ValueError(f"{name} must be [T, {'heads' if heads is None else heads}, {dh}] (got {tuple(t.shape)})")
+    if s2 != 1 or (s1 != dh and h > 1):
+        raise ValueError(f"{name}: the heads of a token must lie one after the other")
+    return t.data_ptr(), (s0 if n > 1 else h * dh)
+
+
+def kv_cache_plan(kv: KVCache, held_len: torch.Tensor, ctx_len: torch.Tensor, new_len: torch.Tensor, table: torch.Tensor,
+                  free_pages: torch.Tensor, n_free: torch.Tensor, n_free_out: torch.Tensor, cu: torch.Tensor,
+                  kv_len: torch.Tensor, pos: torch.Tensor, slot: torch.Tensor, status: torch.Tensor, stream=None):
+    i32, R = torch.int32, held_len.numel()
+    if table.dim() != 2 or table.shape[0] != R:
+        raise ValueError(f"table must be [{R}, max_pages]")
+    T = slot.numel()
+    st = _lib.kv_cache_plan(
+        kv.c, R, table.shape[1], T, _ptr(held_len, "held_len", i32), _ptr(ctx_len, "ctx_len", i32, R),
+        _ptr(new_len, "new_len", i32, R), _ptr(table, "table", i32), _ptr(free_pages, "free_pages", i32, kv.n_pages),
+        _ptr(n_free, "n_free", i32, 1), _ptr(n_free_out, "n_free_out", i32, 1), _ptr(cu, "cu", i32, R + 1),
+        _ptr(kv_len, "kv_len", i32, R), _ptr(pos, "pos", i32, T), _ptr(slot, "slot", i32), _ptr(status, "status", i32, 1),
+        _stream(stream))
+    _check(st, "kv_cache_plan")
+
+
+def kv_cache_append(kv: KVCache, k: torch.Tensor, v: torch.Tensor, slot: torch.Tensor, q: Optional[torch.Tensor] = None,
+                    q_out: Optional[torch.Tensor] = None, pos: Optional[torch.Tensor] = None,
+                    rope: Optional[torch.Tensor] = None, stream=None):
+    T = k.shape[0]
+    if v.shape[0] != T or (q is not None and q.shape[0] != T):
+        raise ValueError("q, k and v must hold the same tokens")
+    kp, ks = _token_rows(k, "k", kv.dtype, kv.h_kv, kv.dh)
+    vp, vs = _token_rows(v, "v", kv.dtype, kv.h_kv, kv.dh)
+    qp, qs, h_q = None, 0, 0
+    if q is not None:
+        h_q = q.shape[1]
+        qp, qs = _token_rows(q, "q", kv.dtype, h_q, kv.dh)
+    n_pos, rot = (0, 0) if rope is None else rope.shape
+    st = _lib.kv_cache_append(
+        kv.c, T, h_q, qp, qs, kp, ks, vp, vs, _ptr(pos, "pos", torch.int32, T), _ptr(slot, "slot", torch.int32, T),
+        _ptr(rope, "rope", torch.float32), n_pos, rot, _ptr(q_out, "q_out", kv.dtype, T * h_q * kv.dh), _stream(stream))
+    _check(st, "kv_cache_append")
+
+
+def kv_cache_attend_workspace_size(kv: KVCache, R: int, T: int, h_q: int, max_new: int, max_len: int) -> int:
+    return int(_lib.kv_cache_attend_workspace_size(kv.c, int(R), int(T), int(h_q), int(max_new), int(max_len)))
+
+
+def kv_cache_attend(kv: KVCache, q: torch.Tensor, table: torch.Tensor, cu: torch.Tensor, kv_len: torch.Tensor,
+                    out: torch.Tensor, ws: torch.Tensor, max_new: int, max_len: int, scale: Optional[float] = None,
+                    window: int = 0, stream=None):
+    i32 = torch.int32
+    T, h_q, _ = q.shape
+    R, max_pages = table.shape
+    qp, qs = _token_rows(q, "q", kv.dtype, h_q, kv.dh)
+    st = _lib.kv_cache_attend(
+        kv.c, R, T, h_q, qp, qs, _ptr(table, "table", i32), max_pages, _ptr(cu, "cu", i32, R + 1),
+        _ptr(kv_len, "kv_len", i32, R), max_new, max_len, kv.dh ** -0.5 if scale is None else scale, window,
+        _ptr(out, "out", kv.dtype, T * h_q * kv.dh), _ptr(ws, "ws"), ws.numel() * ws.element_size(), _stream(stream))
+    _check(st, "kv_cache_attend")
+
+
+def residual_norm(norm: ResidualNorm, h: torch.Tensor, y: Optional[torch.Tensor], h_out: Optional[torch.Tensor],
+                  x_out: Optional[torch.Tensor], gate: Optional[torch.Tensor] = None, stream=None):
+    d = norm.d
+    if h.dtype not in _WDT or (y is not None and y.dtype not in _WDT):
+        raise ValueError("h and y must be bfloat16 or float32")
+    T = h.numel() // d
+    if h.numel() != T * d:
+        raise ValueError(f"h must be [T, {d}]")
+    stride = 0 if gate is None or gate.numel() == d and gate.dim() == 1 else d
+    st = _lib.residual_norm(
+        norm.c, T, _ptr(h, "h"), _WDT[h.dtype], _ptr(y, "y", None, T * d), SFN_F32 if y is None else _WDT[y.dtype],
+        _ptr(gate, "gate", norm.dtype, T * d if stride else d), stride, _ptr(h_out, "h_out", h.dtype, T * d),
+        _ptr(x_out, "x_out", norm.dtype, T * d), _stream(stream))
+    _check(st, "residual_norm")
 
 
 def raw():

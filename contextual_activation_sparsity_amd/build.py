@@ -33,7 +33,8 @@ LIB = os.path.join(PKG, "libsparse_ffn.so")
 SAN_BUILD = os.path.join(BUILD, "san")
 SAN_LIB = os.path.join(SAN_BUILD, "libsparse_ffn_san.so")
 
-SOURCES = ["api.cpp", "decode.hip", "svd_predict.hip", "dense_chunk.hip", "calibrate.hip"]
+SOURCES = ["api.cpp", "decode.hip", "svd_predict.hip", "dense_chunk.hip", "calibrate.hip",
+           "kv_cache.hip", "kv_attend.hip", "residual_norm.hip"]
 ARCH = "gfx950"
 
 COMMON = [

@@ -377,4 +377,211 @@ int ffn_dense_chunk(const sfn_ffn* ffn, const void* x, int32_t n, float* y, void
   }
 }
 
+namespace {
+
+int check_kv(const sfn_kv* kv, bool need_data) {
+  if (!kv) return SFN_EINVAL;
+  if (kv->dtype != SFN_F32 && kv->dtype != SFN_BF16) return SFN_EDTYPE;
+  if (kv->reserved != 0) return SFN_EINVAL;
+  if (kv->page < 16 || kv->page > 256 || (kv->page & (kv->page - 1))) return SFN_ESHAPE;
+  if (kv->n_pages < 1 || (int64_t)kv->n_pages * kv->page > INT32_MAX) return SFN_ESHAPE;
+  if (kv->h_kv < 1 || kv->h_kv > SFN_MAX_HEADS) return SFN_ESHAPE;
+  if (kv->dh != 64 && kv->dh != 128) return SFN_ESHAPE;
+  if (need_data && (!kv->k || !kv->v)) return SFN_EINVAL;
+  if (!aligned16(kv->k) || !aligned16(kv->v)) return SFN_EALIGN;
+  return SFN_OK;
+}
+
+int page_shift(int page) { return __builtin_ctz((unsigned)page); }
+
+// A token stride in elements: room for `heads` heads, 16-byte steps.
+int check_rows(const void* p, int64_t stride, int heads, const sfn_kv* kv) {
+  if (!aligned16(p)) return SFN_EALIGN;
+  if (stride < (int64_t)heads * kv->dh || stride > (int64_t)1 << 32) return SFN_ESHAPE;
+  return stride * wbytes(kv->dtype) % 16 == 0 ? SFN_OK : SFN_EALIGN;
+}
+
+// The shape arguments of an attention call, and its division of the work.
+int check_attend(const sfn_kv* kv, int32_t R, int32_t T, int32_t h_q, int32_t max_new, int32_t max_len) {
+  if (R < 1 || R > SFN_MAX_REQUESTS || T < 0 || T > SFN_MAX_STEP_TOKENS) return SFN_ESHAPE;
+  if (h_q < 1 || h_q > SFN_MAX_HEADS || h_q % kv->h_kv) return SFN_ESHAPE;
+  if (max_new < 1 || max_new > SFN_MAX_STEP_TOKENS || max_len < 0 || max_len > 1 << 30) return SFN_ESHAPE;
+  return SFN_OK;
+}
+
+size_t attend_bytes(const sfn_kv* kv, int32_t T, int32_t h_q, int S) {
+  if (S == 1) return sfn::kWsHeader;
+  const size_t rows = (size_t)T * h_q * S;
+  return sfn::kWsHeader + round256(rows * kv->dh * sizeof(float)) + round256(rows * 2 * sizeof(float));
+}
+
+}  // namespace
+
+int kv_cache_plan(const sfn_kv* kv, int32_t R, int32_t max_pages, int32_t max_tokens, const int32_t* held_len,
+                  const int32_t* ctx_len, const int32_t* new_len, int32_t* table, int32_t* free_pages,
+                  const int32_t* n_free, int32_t* n_free_out, int32_t* cu, int32_t* kv_len, int32_t* pos,
+                  int32_t* slot, int32_t* status, void* stream) {
+  try {
+    const int st = check_kv(kv, false);
+    if (st != SFN_OK) return st;
+    if (R < 1 || R > SFN_MAX_REQUESTS || max_tokens < 1 || max_tokens > SFN_MAX_STEP_TOKENS) return SFN_ESHAPE;
+    if (max_pages < 1 || (int64_t)R * max_pages > INT32_MAX || (int64_t)max_pages * kv->page > INT32_MAX) return SFN_ESHAPE;
+    const void* all[] = {held_len, ctx_len, new_len, table, free_pages, n_free, n_free_out, cu, kv_len, pos, slot, status};
+    for (const void* p : all) {
+      if (!p) return SFN_EINVAL;
+      if (!aligned4_or_null(p)) return SFN_EALIGN;
+    }
+    if (n_free == n_free_out) return SFN_EINVAL;
+    sfn::KvPlanArgs a{held_len, ctx_len, new_len, table, free_pages, n_free, n_free_out, cu, kv_len, pos, slot, status,
+                      R, max_pages, max_tokens, kv->n_pages, page_shift(kv->page)};
+    return hip_status(sfn::launch_kv_plan(a, static_cast<hipStream_t>(stream)));
+  } catch (...) {
+    return SFN_EHIP;
+  }
+}
+
+int kv_cache_append(const sfn_kv* kv, int32_t T, int32_t h_q, const void* q, int64_t q_stride, const void* k,
+                    int64_t k_stride, const void* v, int64_t v_stride, const int32_t* pos, const int32_t* slot,
+                    const float* rope, int32_t n_pos, int32_t rot, void* q_out, void* stream) {
+  try {
+    int st = check_kv(kv, true);
+    if (st != SFN_OK) return st;
+    if (T < 0 || T > SFN_MAX_STEP_TOKENS || h_q < 0 || h_q > SFN_MAX_HEADS) return SFN_ESHAPE;
+    if (T == 0) return SFN_OK;  // empty arrays may have null addresses
+    if ((h_q > 0) != (q != nullptr) || (h_q > 0) != (q_out != nullptr)) return SFN_EINVAL;
+    if (!k || !v || !slot) return SFN_EINVAL;
+    if (rope ? !pos : rot != 0) return SFN_EINVAL;
+    if (rope && (rot < 16 || rot > kv->dh || rot % 16 || n_pos < 1)) return SFN_ESHAPE;
+    if (h_q && (st = check_rows(q, q_stride, h_q, kv)) != SFN_OK) return st;
+    if ((st = check_rows(k, k_stride, kv->h_kv, kv)) != SFN_OK) return st;
+    if ((st = check_rows(v, v_stride, kv->h_kv, kv)) != SFN_OK) return st;
+    if (!aligned16(q_out) || !aligned16(rope) || !aligned4_or_null(pos) || !aligned4_or_null(slot)) return SFN_EALIGN;
+    const int64_t e = wbytes(kv->dtype);
+    sfn::KvAppendArgs a{};
+    a.q = static_cast<const char*>(q);
+    a.k = static_cast<const char*>(k);
+    a.v = static_cast<const char*>(v);
+    a.q_stride = q_stride * e;
+    a.k_stride = k_stride * e;
+    a.v_stride = v_stride * e;
+    a.q_out = static_cast<char*>(q_out);
+    a.k_cache = static_cast<char*>(kv->k);
+    a.v_cache = static_cast<char*>(kv->v);
+    a.pos = pos;
+    a.slot = slot;
+    a.rope = rope;
+    a.T = T;
+    a.h_q = h_q;
+    a.h_kv = kv->h_kv;
+    a.dh = kv->dh;
+    a.rot = rope ? rot : 0;
+    a.n_pos = n_pos;
+    a.n_pages = kv->n_pages;
+    a.page_shift = page_shift(kv->page);
+    return hip_status(sfn::launch_kv_append(a, kv->dtype, static_cast<hipStream_t>(stream)));
+  } catch (...) {
+    return SFN_EHIP;
+  }
+}
+
+size_t kv_cache_attend_workspace_size(const sfn_kv* kv, int32_t R, int32_t T, int32_t h_q, int32_t max_new,
+                                      int32_t max_len) {
+  try {
+    if (check_kv(kv, false) != SFN_OK || check_attend(kv, R, T, h_q, max_new, max_len) != SFN_OK) return 0;
+    return attend_bytes(kv, T, h_q, sfn::attend_plan(R, h_q, kv->h_kv, kv->dtype, max_new, max_len, 0).S_most);
+  } catch (...) {
+    return 0;
+  }
+}
+
+int kv_cache_attend(const sfn_kv* kv, int32_t R, int32_t T, int32_t h_q, const void* q, int64_t q_stride,
+                    const int32_t* table, int32_t max_pages, const int32_t* cu, const int32_t* kv_len,
+                    int32_t max_new, int32_t max_len, float scale, int32_t window, void* out, void* ws,
+                    size_t ws_bytes, void* stream) {
+  try {
+    int st = check_kv(kv, true);
+    if (st != SFN_OK) return st;
+    if ((st = check_attend(kv, R, T, h_q, max_new, max_len)) != SFN_OK) return st;
+    if (max_pages < 1) return SFN_ESHAPE;
+    if ((int64_t)max_pages * kv->page < max_len) max_len = max_pages * kv->page;
+    if (T == 0) return SFN_OK;
+    if (!q || !table || !cu || !kv_len || !out) return SFN_EINVAL;
+    if (!(scale > 0.0f) || !std::isfinite(scale) || window < 0) return SFN_EINVAL;
+    if ((st = check_rows(q, q_stride, h_q, kv)) != SFN_OK) return st;
+    if (!aligned16(out) || !aligned4_or_null(table) || !aligned4_or_null(cu) || !aligned4_or_null(kv_len)) return SFN_EALIGN;
+    const sfn::AttendPlan p = sfn::attend_plan(R, h_q, kv->h_kv, kv->dtype, max_new, max_len, window);
+    if ((int64_t)R * p.S * p.row_tiles * kv->h_kv > INT32_MAX || (int64_t)R * max_new * h_q > INT32_MAX) return SFN_ESHAPE;
+    if ((st = check_ws(ws, ws_bytes, attend_bytes(kv, T, h_q, p.S))) != SFN_OK) return st;
+    sfn::AttendArgs a{};
+    a.k = static_cast<const char*>(kv->k);
+    a.v = static_cast<const char*>(kv->v);
+    a.q = static_cast<const char*>(q);
+    a.q_stride = q_stride * wbytes(kv->dtype);
+    a.table = table;
+    a.cu = cu;
+    a.kv_len = kv_len;
+    a.out = static_cast<char*>(out);
+    if (p.S > 1) {
+      char* w = static_cast<char*>(ws) + sfn::kWsHeader;
+      a.part_o = reinterpret_cast<float*>(w);
+      a.part_ml = reinterpret_cast<float*>(w + round256((size_t)T * h_q * p.S * kv->dh * sizeof(float)));
+    }
+    a.R = R;
+    a.T = T;
+    a.h_q = h_q;
+    a.h_kv = kv->h_kv;
+    a.g = h_q / kv->h_kv;
+    a.page_shift = page_shift(kv->page);
+    a.n_pages = kv->n_pages;
+    a.max_pages = max_pages;
+    a.max_new = max_new;
+    a.max_len = max_len;
+    a.window = window;
+    a.row_tiles = p.row_tiles;
+    a.S = p.S;
+    a.chunk = p.chunk;
+    a.scale_log2 = scale * 1.44269504088896340736f;
+    return hip_status(sfn::launch_kv_attend(a, p.RT, kv->dh, kv->dtype, static_cast<hipStream_t>(stream)));
+  } catch (...) {
+    return SFN_EHIP;
+  }
+}
+
+int residual_norm(const sfn_norm* norm, int32_t T, const void* h, int32_t hdtype, const void* y, int32_t ydtype,
+                  const void* gate, int64_t gate_stride, void* h_out, void* x_out, void* stream) {
+  try {
+    if (!norm) return SFN_EINVAL;
+    for (int dt : {norm->wdtype, hdtype, ydtype})
+      if (dt != SFN_F32 && dt != SFN_BF16) return SFN_EDTYPE;
+    if (norm->d < 8 || norm->d > SFN_MAX_D || T < 0 || T > SFN_MAX_STEP_TOKENS) return SFN_ESHAPE;
+    if (norm->d % 8) return SFN_EALIGN;
+    if (T == 0) return SFN_OK;
+    if (!(norm->eps >= 0.0f) || !std::isfinite(norm->eps) || !std::isfinite(norm->scale)) return SFN_EINVAL;
+    if (!h || (!h_out && !x_out)) return SFN_EINVAL;
+    if (x_out && !norm->w_pre) return SFN_EINVAL;
+    if (!y && (h_out || gate)) return SFN_EINVAL;
+    if (gate && gate_stride != 0 && gate_stride < norm->d) return SFN_ESHAPE;
+    if (gate && gate_stride % 8) return SFN_EALIGN;
+    const void* all[] = {h, y, gate, h_out, x_out, norm->w_post, norm->w_pre};
+    for (const void* p : all)
+      if (!aligned16(p)) return SFN_EALIGN;
+    sfn::NormArgs a{};
+    a.h = static_cast<const char*>(h);
+    a.y = static_cast<const char*>(y);
+    a.w_post = static_cast<const char*>(norm->w_post);
+    a.w_pre = static_cast<const char*>(norm->w_pre);
+    a.gate = static_cast<const char*>(gate);
+    a.gate_stride = gate_stride * wbytes(norm->wdtype);
+    a.h_out = static_cast<char*>(h_out);
+    a.x_out = static_cast<char*>(x_out);
+    a.scale = norm->scale;
+    a.eps = norm->eps;
+    a.T = T;
+    a.d = norm->d;
+    return hip_status(sfn::launch_residual_norm(a, hdtype, ydtype, norm->wdtype, static_cast<hipStream_t>(stream)));
+  } catch (...) {
+    return SFN_EHIP;
+  }
+}
+
 }  // extern "C"

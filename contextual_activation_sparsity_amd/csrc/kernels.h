@@ -91,4 +91,52 @@ hipError_t launch_svd_z(const sfn_svd& s, const void* x, float* z, hipStream_t s
 hipError_t launch_svd_predict(const sfn_svd& s, const void* x, int32_t* cand, int32_t* n_cand, float* p_out,
                               void* ws, hipStream_t stream);
 
+// ---- paged key/value cache and residual norm ------------------------------------------
+
+struct KvPlanArgs {
+  const int32_t *held, *ctx, *fresh;  // [R]
+  int32_t* table;                     // [R, max_pages]
+  int32_t* free_pages;                // [n_pages]
+  const int32_t* n_free;
+  int32_t *n_free_out, *cu, *kv_len, *pos, *slot, *status;
+  int R, max_pages, max_tokens, n_pages, page_shift;
+};
+hipError_t launch_kv_plan(const KvPlanArgs& a, hipStream_t stream);
+
+struct KvAppendArgs {
+  const char *q, *k, *v;
+  int64_t q_stride, k_stride, v_stride;  // bytes from token to token
+  char *q_out, *k_cache, *v_cache;
+  const int32_t *pos, *slot;
+  const float* rope;  // [n_pos, rot]
+  int T, h_q, h_kv, dh, rot, n_pos, n_pages, page_shift;
+};
+hipError_t launch_kv_append(const KvAppendArgs& a, int dtype, hipStream_t stream);
+
+struct AttendArgs {
+  const char *k, *v, *q;
+  int64_t q_stride;  // bytes from token to token
+  const int32_t *table, *cu, *kv_len;
+  char* out;
+  float *part_o, *part_ml;  // [T, h_q, S, dh] and [T, h_q, S, 2], or null (S = 1)
+  int R, T, h_q, h_kv, g, page_shift, n_pages, max_pages, max_new, max_len, window;
+  int row_tiles, S, chunk;
+  float scale_log2;  // score scale times log2(e)
+};
+struct AttendPlan {
+  int RT, row_tiles, S, chunk;
+  int S_most;  // the largest S for these arguments and any window
+};
+AttendPlan attend_plan(int R, int h_q, int h_kv, int dtype, int max_new, int max_len, int window);
+hipError_t launch_kv_attend(const AttendArgs& a, int RT, int dh, int dtype, hipStream_t stream);
+
+struct NormArgs {
+  const char *h, *y, *w_post, *w_pre, *gate;
+  int64_t gate_stride;  // bytes from token to token (0: one vector for all)
+  char *h_out, *x_out;
+  float scale, eps;
+  int T, d;
+};
+hipError_t launch_residual_norm(const NormArgs& a, int hdtype, int ydtype, int wdtype, hipStream_t stream);
+
 }  // namespace sfn

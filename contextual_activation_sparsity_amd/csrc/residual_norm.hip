@@ -1,0 +1,165 @@
+// The update of the residual stream between two blocks, with the norms on either side of
+// it: h_out = h + scale gate N(y; w_post), x_out = N(h_out; w_pre), N(v; w) =
+// v / sqrt(mean(v^2) + eps) w. One workgroup per token holds the row in registers, so
+// every input is read once and every output written once, with the two sums of squares
+// (fp32) between. x_out is computed from the fp32 row, before h_out is rounded: each
+// output is rounded once. HBM bound for many tokens; for one token, the launch, one round
+// of loads and two workgroup-wide sums.
+
+#include "device_common.h"
+#include "kernels.h"
+#include "sparse_ffn.h"
+
+namespace sfn {
+
+namespace {
+
+constexpr int kNormVals = 8;  // values a thread handles together
+
+template <int WT>
+__device__ __forceinline__ void load8(const SFN_GLOBAL char* p, int64_t i, float* f) {
+  if constexpr (WT == WT_BF16) {
+    const uint4 v = ld16(p + i * 16);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      f[2 * j] = __uint_as_float(w[j] << 16);
+      f[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+    }
+  } else {
+    const uint4 a = ld16(p + i * 32), b = ld16(p + i * 32 + 16);
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = __uint_as_float(w[j]);
+  }
+}
+
+template <int WT>
+__device__ __forceinline__ void store8(SFN_GLOBAL char* p, int64_t i, const float* f) {
+  if constexpr (WT == WT_BF16) {
+    *reinterpret_cast<SFN_GLOBAL u32x4_t*>(p + i * 16) =
+        u32x4_t{pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7])};
+  } else {
+    *reinterpret_cast<SFN_GLOBAL f32x4_t*>(p + i * 32) = f32x4_t{f[0], f[1], f[2], f[3]};
+    *reinterpret_cast<SFN_GLOBAL f32x4_t*>(p + i * 32 + 16) = f32x4_t{f[4], f[5], f[6], f[7]};
+  }
+}
+
+template <int NT>
+__device__ __forceinline__ float block_sum(float v, float* s_part) {
+  v = wave_sum(v);
+  if constexpr (NT == 64) return v;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  __syncthreads();  // the previous sum has been read
+  if (lane == 0) s_part[wave] = v;
+  __syncthreads();
+  float t = 0.f;
+#pragma unroll
+  for (int w = 0; w < NT / 64; ++w) t += s_part[w];
+  return t;
+}
+
+template <int HT, int YT, int WT, int NT, int NV>
+__global__ __launch_bounds__(NT) void residual_norm_kernel(NormArgs a) {
+  __shared__ float s_part[NT / 64];
+  const int t = blockIdx.x, tid = threadIdx.x;
+  const int nch = a.d / kNormVals;
+  const int64_t row = (int64_t)t * nch;
+  const float inv_d = 1.0f / (float)a.d;
+  float h[NV][kNormVals];
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int i = tid + v * NT;
+    if (i < nch) load8<HT>(gp(a.h), row + i, h[v]);
+    else
+#pragma unroll
+      for (int j = 0; j < kNormVals; ++j) h[v][j] = 0.f;
+  }
+  if (a.y) {
+    float y[NV][kNormVals];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int i = tid + v * NT;
+      if (i < nch) load8<YT>(gp(a.y), row + i, y[v]);
+      else
+#pragma unroll
+        for (int j = 0; j < kNormVals; ++j) y[v][j] = 0.f;
+    }
+    float s = 1.f;
+    if (a.w_post) {
+      float q = 0.f;
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int j = 0; j < kNormVals; ++j) q = fmaf(y[v][j], y[v][j], q);
+      q = block_sum<NT>(q, s_part);
+      s = 1.0f / sqrtf(fmaf(q, inv_d, a.eps));
+    }
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int i = tid + v * NT;
+      if (i >= nch) continue;
+      if (a.w_post) {
+        float w[kNormVals];
+        load8<WT>(gp(a.w_post), i, w);
+#pragma unroll
+        for (int j = 0; j < kNormVals; ++j) y[v][j] = y[v][j] * s * w[j];
+      }
+      if (a.gate) {
+        float g[kNormVals];
+        load8<WT>(gp(a.gate) + (int64_t)t * a.gate_stride, i, g);
+#pragma unroll
+        for (int j = 0; j < kNormVals; ++j) y[v][j] *= g[j];
+      }
+#pragma unroll
+      for (int j = 0; j < kNormVals; ++j) h[v][j] = fmaf(a.scale, y[v][j], h[v][j]);
+      if (a.h_out) store8<HT>(gp(a.h_out), row + i, h[v]);
+    }
+  }
+  if (!a.x_out) return;
+  float q = 0.f;
+#pragma unroll
+  for (int v = 0; v < NV; ++v)
+#pragma unroll
+    for (int j = 0; j < kNormVals; ++j) q = fmaf(h[v][j], h[v][j], q);
+  q = block_sum<NT>(q, s_part);
+  const float s = 1.0f / sqrtf(fmaf(q, inv_d, a.eps));
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int i = tid + v * NT;
+    if (i >= nch) continue;
+    float w[kNormVals];
+    load8<WT>(gp(a.w_pre), i, w);
+#pragma unroll
+    for (int j = 0; j < kNormVals; ++j) w[j] = h[v][j] * s * w[j];
+    store8<WT>(gp(a.x_out), row + i, w);
+  }
+}
+
+template <int HT, int YT, int WT>
+void launch_sized(const NormArgs& a, hipStream_t stream) {
+  const int nch = a.d / kNormVals;
+  if (nch <= 256) hipLaunchKernelGGL((residual_norm_kernel<HT, YT, WT, 256, 1>), dim3(a.T), dim3(256), 0, stream, a);
+  else if (nch <= 512) hipLaunchKernelGGL((residual_norm_kernel<HT, YT, WT, 256, 2>), dim3(a.T), dim3(256), 0, stream, a);
+  else if (nch <= 1024) hipLaunchKernelGGL((residual_norm_kernel<HT, YT, WT, 512, 2>), dim3(a.T), dim3(512), 0, stream, a);
+  else hipLaunchKernelGGL((residual_norm_kernel<HT, YT, WT, 1024, 2>), dim3(a.T), dim3(1024), 0, stream, a);
+}
+
+}  // namespace
+
+hipError_t launch_residual_norm(const NormArgs& a, int hdtype, int ydtype, int wdtype, hipStream_t stream) {
+  const int k = (hdtype == SFN_BF16 ? 4 : 0) | (ydtype == SFN_BF16 ? 2 : 0) | (wdtype == SFN_BF16 ? 1 : 0);
+  switch (k) {
+    case 0: launch_sized<WT_F32, WT_F32, WT_F32>(a, stream); break;
+    case 1: launch_sized<WT_F32, WT_F32, WT_BF16>(a, stream); break;
+    case 2: launch_sized<WT_F32, WT_BF16, WT_F32>(a, stream); break;
+    case 3: launch_sized<WT_F32, WT_BF16, WT_BF16>(a, stream); break;
+    case 4: launch_sized<WT_BF16, WT_F32, WT_F32>(a, stream); break;
+    case 5: launch_sized<WT_BF16, WT_F32, WT_BF16>(a, stream); break;
+    case 6: launch_sized<WT_BF16, WT_BF16, WT_F32>(a, stream); break;
+    default: launch_sized<WT_BF16, WT_BF16, WT_BF16>(a, stream); break;
+  }
+  return hipGetLastError();
+}
+
+}  // namespace sfn

@@ -102,6 +102,9 @@ extern "C" {
 #define SFN_MAX_D 16384
 #define SFN_MAX_F 262144
 #define SFN_MAX_RANK 1024 /* SVD predictor rank */
+#define SFN_MAX_REQUESTS 4096      /* requests of one step over the paged cache */
+#define SFN_MAX_STEP_TOKENS 262144 /* tokens of one step over the paged cache */
+#define SFN_MAX_HEADS 1024         /* query heads, and key/value heads */
 
 /* One FFN layer. All pointers device, each matrix [f, d] row-major in `wdtype`. */
 typedef struct sfn_ffn {
@@ -273,6 +276,134 @@ int sparse_ffn_decode_svd(const sfn_ffn* ffn, const sfn_svd* svd, const void* x,
  */
 int ffn_dense_chunk(const sfn_ffn* ffn, const void* x, int32_t n, float* y, void* ws,
                     size_t ws_bytes, void* stream);
+
+/*
+ * ---- The paged key/value cache of the layer's attention, and the residual norm ---------
+ *
+ * What stands between two sparse FFN steps in a decoder layer. A step serves R requests at
+ * once, each with any number of new tokens: one (decoding), a chunk (the verification of
+ * up to 16 sparse-generated tokens, whose rejected ones the next plan drops again), or a
+ * prompt. The new tokens of all requests lie one after the other, T of them: request r's
+ * are [cu[r], cu[r + 1]).
+ *
+ * The calls of a step: kv_cache_plan once (lengths to pages, slots and positions), then for
+ * each layer kv_cache_append and kv_cache_attend, with residual_norm around the blocks. All
+ * lengths, tables and slots stay on the device; the host gives upper bounds, so a step can
+ * be captured in a graph and replayed with other lengths. The conventions above hold; the
+ * plan, the append and the norm need no workspace.
+ */
+
+/* The cache of one layer. A page holds `page` tokens of one request, for all its heads;
+ * which pages a request holds, in order, is its row of the page table. k and v may be NULL
+ * for kv_cache_plan, which reads the shape alone (every layer shares one plan). */
+typedef struct sfn_kv {
+  int32_t n_pages;  /* pages; n_pages * page <= 2^31 - 1 */
+  int32_t page;     /* tokens to a page: 16, 32, 64, 128 or 256 */
+  int32_t h_kv;     /* key/value heads */
+  int32_t dh;       /* values of a head: 64 or 128 */
+  int32_t dtype;    /* SFN_F32 or SFN_BF16 */
+  int32_t reserved; /* must be 0 */
+  void* k;          /* [n_pages, h_kv, page, dh] */
+  void* v;          /* [n_pages, h_kv, page, dh] */
+} sfn_kv;
+
+/*
+ * Plans one step: gives every new token its place, takes pages from a stack of free ones
+ * and gives back those that shorter requests no longer need. With p = page, request r
+ * holds ceil(held_len / p) pages and needs ceil((ctx_len + new_len) / p):
+ *   - pages past what it needs are pushed on the stack, in request order, ascending index;
+ *   - then pages are popped for those that need more, in request order, ascending index;
+ *   - its token i has position ctx_len + i and slot table[r][pos / p] * p + pos % p.
+ * ctx_len < held_len drops tokens (rejected drafts); ctx_len = new_len = 0 gives back all.
+ * The next step's held_len is this step's kv_len.
+ *   held_len, ctx_len, new_len  [R]: tokens the pages were taken for, tokens kept of them
+ *              (<= held_len), new tokens
+ *   table      [R, max_pages]: in, the held pages; out, with the taken pages written;
+ *              entries past the needed ones are not cleared
+ *   free_pages [n_pages]: the stack, its first *n_free entries free; pushed pages written
+ *   n_free     1 int32, read;  n_free_out  1 int32, written (not the same address)
+ *   cu         [R + 1], kv_len [R] (ctx_len + new_len), written
+ *   pos, slot  [max_tokens], written: past the last token 0 and -1
+ *   status     1 int32, written: 0; the number of pages missing; or -1 for lengths that
+ *              are negative, longer than a table row or than held_len, more than max_tokens
+ *              tokens, or a stack that would outgrow n_pages. Unless 0 nothing is taken or
+ *              given back (table and stack unchanged, *n_free_out = *n_free), cu and kv_len
+ *              are 0 and every slot -1, so the calls after it write and attend to nothing.
+ * Planning the same inputs again gives the same result. R <= 4096, max_tokens <= 262144.
+ */
+int kv_cache_plan(const sfn_kv* kv, int32_t R, int32_t max_pages, int32_t max_tokens, const int32_t* held_len,
+                  const int32_t* ctx_len, const int32_t* new_len, int32_t* table, int32_t* free_pages,
+                  const int32_t* n_free, int32_t* n_free_out, int32_t* cu, int32_t* kv_len, int32_t* pos,
+                  int32_t* slot, int32_t* status, void* stream);
+
+/*
+ * Rotates the new tokens' queries and keys to their positions and writes keys and values
+ * into the cache. Of each head the first `rot` values are turned, value i together with
+ * value i + rot / 2: (a, b) -> (a c - b s, b c + a s) with c and s from row pos of `rope`;
+ * the rest, and all of v, is copied. bf16 values are turned in fp32 and rounded once.
+ *   q, k, v  token t's heads at q + t * q_stride (elements; so the three may be parts of
+ *            one projection's output), each head's dh values contiguous, in kv->dtype;
+ *            addresses and strides 16-byte aligned. q NULL (h_q 0, q_out NULL): no queries
+ *   pos      [T], clamped into [0, n_pos) (NULL without rope)
+ *   slot     [T]; a token whose slot is outside the cache writes no key and no value. Slots
+ *            of one call are distinct
+ *   rope     [n_pos, rot] fp32, a row's rot / 2 cosines, then its sines; NULL: no rotation
+ *   rot      0 without rope, else a multiple of 16, at most dh
+ *   q_out    [T, h_q, dh], written; may be q itself where q_stride is h_q * dh
+ * T = 0 does nothing.
+ */
+int kv_cache_append(const sfn_kv* kv, int32_t T, int32_t h_q, const void* q, int64_t q_stride, const void* k,
+                    int64_t k_stride, const void* v, int64_t v_stride, const int32_t* pos, const int32_t* slot,
+                    const float* rope, int32_t n_pos, int32_t rot, void* q_out, void* stream);
+
+/*
+ * Attention of the new tokens over the cache (which holds their own keys and values
+ * already). Token i of the n new tokens of request r is at position P = kv_len - n + i:
+ *   out = sum_j w_j v_j, w = softmax_j(scale q.k_j) over the keys j <= P, and with a window
+ *   W > 0 only those with j > P - W,
+ * query head h reading key head h / (h_q / h_kv). A token that sees no key (kv_len < n)
+ * gives zeros. What a page holds past kv_len is not used, whatever it is. Scores, softmax
+ * and sums are fp32; for bf16 the weights are rounded to bf16 before they multiply v.
+ *   q        as in kv_cache_append (after it: its q_out);  out [T, h_q, dh]
+ *   table    [R, max_pages] (entries are clamped into [0, n_pages)), cu [R + 1], kv_len [R]
+ *   max_new, max_len  bounds on every request's new tokens and kv_len (up to 2^30): tokens
+ *            past max_new are not computed, keys past max_len or past the table row not read
+ *   scale    > 0;  window >= 0 (0: none)
+ * Workspace: kv_cache_attend_workspace_size bytes for the same arguments (0 on invalid
+ * ones). T = 0 does nothing. Results do not depend on what else runs.
+ */
+size_t kv_cache_attend_workspace_size(const sfn_kv* kv, int32_t R, int32_t T, int32_t h_q, int32_t max_new,
+                                      int32_t max_len);
+int kv_cache_attend(const sfn_kv* kv, int32_t R, int32_t T, int32_t h_q, const void* q, int64_t q_stride,
+                    const int32_t* table, int32_t max_pages, const int32_t* cu, const int32_t* kv_len,
+                    int32_t max_new, int32_t max_len, float scale, int32_t window, void* out, void* ws,
+                    size_t ws_bytes, void* stream);
+
+/* The norms on either side of the residual stream's update. All pointers device. */
+typedef struct sfn_norm {
+  int32_t d;          /* hidden size, a multiple of 8, at most SFN_MAX_D */
+  int32_t wdtype;     /* dtype of w_post, w_pre, gate and x_out */
+  float eps;          /* >= 0 */
+  float scale;        /* the residual scale */
+  const void* w_post; /* [d]: norm of the block's output, or NULL for none */
+  const void* w_pre;  /* [d]: norm of the new residual, or NULL (then x_out must be NULL) */
+} sfn_norm;
+
+/*
+ * Adds a block's output to the residual stream and makes the next block's input:
+ *   h_out = h + scale * gate * N(y; w_post)      x_out = N(h_out; w_pre)
+ *   N(v; w) = v / sqrt(mean(v^2) + eps) * w      (N(y) = y without w_post, gate 1 without)
+ * computed in fp32, x_out from h_out before it is rounded.
+ *   h      [T, d] in hdtype;  h_out the same, and may be h itself
+ *   y      [T, d] in ydtype (the FFN's fp32, or bf16), or NULL: x_out = N(h; w_pre) alone
+ *          (the first block), h_out NULL
+ *   gate   [d] with gate_stride 0, or [T, d] with gate_stride elements from token to token
+ *          (a multiple of 8); in wdtype; NULL for none
+ *   x_out  [T, d] in wdtype, or NULL;  must not overlap h or y
+ * T = 0 does nothing. Rows 16-byte aligned.
+ */
+int residual_norm(const sfn_norm* norm, int32_t T, const void* h, int32_t hdtype, const void* y, int32_t ydtype,
+                  const void* gate, int64_t gate_stride, void* h_out, void* x_out, void* stream);
 
 #ifdef __cplusplus
 }
