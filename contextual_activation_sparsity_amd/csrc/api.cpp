@@ -537,11 +537,13 @@ int kv_cache_attend(const sfn_kv* kv, int32_t R, int32_t T, int32_t h_q, const v
     a.max_new = max_new;
     a.max_len = max_len;
     a.window = window;
+    a.tile_rows = p.tile_rows;
+    a.tile_keys = p.tile_keys;
     a.row_tiles = p.row_tiles;
     a.S = p.S;
     a.chunk = p.chunk;
     a.scale_log2 = scale * 1.44269504088896340736f;
-    return hip_status(sfn::launch_kv_attend(a, p.RT, kv->dh, kv->dtype, static_cast<hipStream_t>(stream)));
+    return hip_status(sfn::launch_kv_attend(a, kv->dh, kv->dtype, static_cast<hipStream_t>(stream)));
   } catch (...) {
     return SFN_EHIP;
   }

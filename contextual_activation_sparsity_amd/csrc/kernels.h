@@ -120,15 +120,16 @@ struct AttendArgs {
   char* out;
   float *part_o, *part_ml;  // [T, h_q, S, dh] and [T, h_q, S, 2], or null (S = 1)
   int R, T, h_q, h_kv, g, page_shift, n_pages, max_pages, max_new, max_len, window;
-  int row_tiles, S, chunk;
+  int tile_rows, tile_keys, row_tiles, S, chunk;  // see AttendPlan
   float scale_log2;  // score scale times log2(e)
 };
 struct AttendPlan {
-  int RT, row_tiles, S, chunk;
+  int tile_rows, tile_keys;  // query rows of a workgroup, keys it takes at a time
+  int row_tiles, S, chunk;   // workgroups for a key head's rows and keys, keys of a split
   int S_most;  // the largest S for these arguments and any window
 };
 AttendPlan attend_plan(int R, int h_q, int h_kv, int dtype, int max_new, int max_len, int window);
-hipError_t launch_kv_attend(const AttendArgs& a, int RT, int dh, int dtype, hipStream_t stream);
+hipError_t launch_kv_attend(const AttendArgs& a, int dh, int dtype, hipStream_t stream);
 
 struct NormArgs {
   const char *h, *y, *w_post, *w_pre, *gate;
