@@ -409,10 +409,8 @@ int check_attend(const sfn_kv* kv, int32_t R, int32_t T, int32_t h_q, int32_t ma
   return SFN_OK;
 }
 
-size_t attend_bytes(const sfn_kv* kv, int32_t T, int32_t h_q, int S) {
-  if (S == 1) return sfn::kWsHeader;
-  const size_t rows = (size_t)T * h_q * S;
-  return sfn::kWsHeader + round256(rows * kv->dh * sizeof(float)) + round256(rows * 2 * sizeof(float));
+size_t attend_bytes(const sfn_kv* kv, const sfn::AttendPlan& p) {
+  return sfn::kWsHeader + round256((size_t)p.parts * kv->dh * sizeof(float)) + round256((size_t)p.parts * 2 * sizeof(float));
 }
 
 }  // namespace
@@ -488,7 +486,7 @@ size_t kv_cache_attend_workspace_size(const sfn_kv* kv, int32_t R, int32_t T, in
                                       int32_t max_len) {
   try {
     if (check_kv(kv, false) != SFN_OK || check_attend(kv, R, T, h_q, max_new, max_len) != SFN_OK) return 0;
-    return attend_bytes(kv, T, h_q, sfn::attend_plan(R, h_q, kv->h_kv, kv->dtype, max_new, max_len, 0).S_most);
+    return attend_bytes(kv, sfn::attend_plan(R, h_q, kv->h_kv, kv->dtype, max_new, max_len, 0));
   } catch (...) {
     return 0;
   }
@@ -509,9 +507,10 @@ int kv_cache_attend(const sfn_kv* kv, int32_t R, int32_t T, int32_t h_q, const v
     if (!(scale > 0.0f) || !std::isfinite(scale) || window < 0) return SFN_EINVAL;
     if ((st = check_rows(q, q_stride, h_q, kv)) != SFN_OK) return st;
     if (!aligned16(out) || !aligned4_or_null(table) || !aligned4_or_null(cu) || !aligned4_or_null(kv_len)) return SFN_EALIGN;
+    if (window >= max_len) window = 0;  // every key is within it
     const sfn::AttendPlan p = sfn::attend_plan(R, h_q, kv->h_kv, kv->dtype, max_new, max_len, window);
     if ((int64_t)R * p.S * p.row_tiles * kv->h_kv > INT32_MAX || (int64_t)R * max_new * h_q > INT32_MAX) return SFN_ESHAPE;
-    if ((st = check_ws(ws, ws_bytes, attend_bytes(kv, T, h_q, p.S))) != SFN_OK) return st;
+    if ((st = check_ws(ws, ws_bytes, attend_bytes(kv, p))) != SFN_OK) return st;
     sfn::AttendArgs a{};
     a.k = static_cast<const char*>(kv->k);
     a.v = static_cast<const char*>(kv->v);
@@ -521,16 +520,15 @@ int kv_cache_attend(const sfn_kv* kv, int32_t R, int32_t T, int32_t h_q, const v
     a.cu = cu;
     a.kv_len = kv_len;
     a.out = static_cast<char*>(out);
-    if (p.S > 1) {
-      char* w = static_cast<char*>(ws) + sfn::kWsHeader;
-      a.part_o = reinterpret_cast<float*>(w);
-      a.part_ml = reinterpret_cast<float*>(w + round256((size_t)T * h_q * p.S * kv->dh * sizeof(float)));
-    }
+    char* w = static_cast<char*>(ws) + sfn::kWsHeader;
+    a.part_o = reinterpret_cast<float*>(w);
+    a.part_ml = reinterpret_cast<float*>(w + round256((size_t)p.parts * kv->dh * sizeof(float)));
     a.R = R;
     a.T = T;
     a.h_q = h_q;
     a.h_kv = kv->h_kv;
     a.g = h_q / kv->h_kv;
+    a.g_mul = ((1 << 21) + a.g - 1) / a.g;
     a.page_shift = page_shift(kv->page);
     a.n_pages = kv->n_pages;
     a.max_pages = max_pages;

@@ -118,15 +118,15 @@ struct AttendArgs {
   int64_t q_stride;  // bytes from token to token
   const int32_t *table, *cu, *kv_len;
   char* out;
-  float *part_o, *part_ml;  // [T, h_q, S, dh] and [T, h_q, S, 2], or null (S = 1)
-  int R, T, h_q, h_kv, g, page_shift, n_pages, max_pages, max_new, max_len, window;
+  float *part_o, *part_ml;  // [R, max_new, h_q, S, dh] and [R, max_new, h_q, S, 2] (S > 1)
+  int R, T, h_q, h_kv, g, g_mul, page_shift, n_pages, max_pages, max_new, max_len, window;
   int tile_rows, tile_keys, row_tiles, S, chunk;  // see AttendPlan
-  float scale_log2;  // score scale times log2(e)
-};
+  float scale_log2;                               // score scale times log2(e)
+};  // g = h_q / h_kv, g_mul = ceil(2^21 / g)
 struct AttendPlan {
   int tile_rows, tile_keys;  // query rows of a workgroup, keys it takes at a time
-  int row_tiles, S, chunk;   // workgroups for a key head's rows and keys, keys of a split
-  int S_most;  // the largest S for these arguments and any window
+  int row_tiles, S, chunk;   // workgroups for a key head's rows and for its keys, keys of a split
+  int64_t parts;             // rows of partial results
 };
 AttendPlan attend_plan(int R, int h_q, int h_kv, int dtype, int max_new, int max_len, int window);
 hipError_t launch_kv_attend(const AttendArgs& a, int dh, int dtype, hipStream_t stream);

@@ -14,6 +14,7 @@ namespace {
 typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8_t;
 
 constexpr float kNegInf = -__builtin_huge_valf();
+constexpr int kMaxSplits = 256;  // the join kernel's threads
 
 // ---- split attention -----------------------------------------------------------------
 //
@@ -45,6 +46,29 @@ struct AttnTile {
   static constexpr int NB = DH / (16 * VW);        // times that
   static constexpr int NO = DH / 16;               // output blocks
 };
+
+typedef __attribute__((ext_vector_type(2))) float f32x2_t;
+
+// Values d4 .. d4 + 3 of one output row, from their unscaled sums and the sum of weights.
+template <int WT, int DH>
+__device__ __forceinline__ void store_row(const AttendArgs& a, int token, int head, int d4, f32x4_t o, float L) {
+  o *= L == 0.f ? 0.f : 1.0f / L;
+  const int64_t at = ((int64_t)token * a.h_q + head) * DH + d4;
+  if constexpr (WT == WT_BF16)
+    *reinterpret_cast<SFN_GLOBAL uint64_t*>(gp(a.out) + at * 2) =
+        (uint64_t)pack_bf16(o[0], o[1]) | (uint64_t)pack_bf16(o[2], o[3]) << 32;
+  else
+    *reinterpret_cast<SFN_GLOBAL f32x4_t*>(gp(a.out) + at * 4) = o;
+}
+
+__device__ __forceinline__ float wave_max(float v) {
+  v = fmaxf(v, dpp_mov<SFN_DPP_XOR1>(v));
+  v = fmaxf(v, dpp_mov<SFN_DPP_XOR2>(v));
+  v = fmaxf(v, dpp_mov<SFN_DPP_HALF_MIRROR>(v));
+  v = fmaxf(v, dpp_mov<SFN_DPP_ROW_MIRROR>(v));
+  v = swap_pair_max<16>(v);
+  return swap_pair_max<32>(v);
+}
 
 // Whether a word holds a value that is not finite (fp32, or either bf16 half).
 template <int WT>
@@ -110,6 +134,7 @@ __device__ __forceinline__ void add_one_key(const SFN_GLOBAL char* vp, const f32
 #pragma unroll
     for (int i = 0; i < 4; ++i) w = 16 * u + i == kk - 4 * q ? p[u][i] : w;
   const bool mine = (kk >> 2 & 3) == q;
+  asm("" : "+v"(vp));  // no address of this is kept through the main loop
 #pragma unroll
   for (int nb = 0; nb < C::NB; ++nb) {
 #pragma unroll
@@ -132,58 +157,161 @@ __device__ __forceinline__ void add_one_key(const SFN_GLOBAL char* vp, const f32
   }
 }
 
-template <int WT, int DH, int RT>
-__global__ __launch_bounds__(256, RT == 1 ? 3 : RT == 2 ? 2 : 1) void attend_split_kernel(AttendArgs a) {
+// One tile of keys in a lane's registers.
+template <int WT, int DH>
+struct KeyTile {
+  using C = AttnTile<WT, DH>;
+  uint4 k[C::NG][C::NQ];
+  uint32_t v[C::NG][4][C::NB][C::VW * C::KB / 4];
+
+  // row: the cache row of each group's first key
+  __device__ __forceinline__ void load(const AttendArgs& a, const int64_t (&row)[C::NG], int c, int q) {
+    constexpr int ROW = DH * C::KB;
+#pragma unroll
+    for (int u = 0; u < C::NG; ++u) {
+      const SFN_GLOBAL char* kp = gp(a.k) + (row[u] + c) * ROW + 16 * q;
+#pragma unroll
+      for (int s = 0; s < C::NQ; ++s) k[u][s] = ldg16(kp + 64 * s);
+    }
+#pragma unroll
+    for (int u = 0; u < C::NG; ++u) {
+      const SFN_GLOBAL char* vp = gp(a.v) + (row[u] + 4 * q) * ROW + c * C::VW * C::KB;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int nb = 0; nb < C::NB; ++nb) {
+          const SFN_GLOBAL char* p = vp + j * ROW + nb * 16 * C::VW * C::KB;
+          if constexpr (C::VW * C::KB == 16) {
+            const uint4 w = ldg16(p);
+            v[u][j][nb][0] = w.x;
+            v[u][j][nb][1] = w.y;
+            v[u][j][nb][2] = w.z;
+            v[u][j][nb][3] = w.w;
+          } else {
+            const uint64_t w = __builtin_nontemporal_load(reinterpret_cast<const SFN_GLOBAL uint64_t*>(p));
+            v[u][j][nb][0] = (uint32_t)w;
+            v[u][j][nb][1] = (uint32_t)(w >> 32);
+          }
+        }
+    }
+  }
+
+  // Zeroes the values of keys from `keys` on (keys of the tile that the sequence has); returns
+  // whether some other value is not finite, and makes those 0 too.
+  __device__ __forceinline__ bool clean(int keys, int q) {
+    uint32_t top = 0;  // the largest magnitude bits seen: of the bf16 halves, or of the fp32 words
+#pragma unroll
+    for (int u = 0; u < C::NG; ++u)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int nb = 0; nb < C::NB; ++nb)
+#pragma unroll
+          for (int w = 0; w < C::VW * C::KB / 4; ++w) {
+            uint32_t& x = v[u][j][nb][w];
+            x = 16 * u + j < keys - 4 * q ? x : 0u;
+            if constexpr (C::kBf) {
+              typedef __attribute__((ext_vector_type(2))) uint16_t u16x2_t;
+              top = __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2_t, top),
+                                                                           __builtin_bit_cast(u16x2_t, x & 0x7fff7fffu)));
+            } else {
+              top = max(top, x & 0x7fffffffu);
+            }
+          }
+    const bool odd = C::kBf ? (top & 0xffffu) >= 0x7f80u || top >= 0x7f800000u : top >= 0x7f800000u;
+    if (!__any(odd)) return false;
+#pragma unroll
+    for (int u = 0; u < C::NG; ++u)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int nb = 0; nb < C::NB; ++nb)
+#pragma unroll
+          for (int w = 0; w < C::VW * C::KB / 4; ++w) v[u][j][nb][w] = finite_part<WT>(v[u][j][nb][w]);
+    return true;
+  }
+};
+
+// The rows of a tile that starts at row rho0: which token and which of the g heads.
+struct RowMap {
+  int tok0, rem0, mul, g;
+  __device__ __forceinline__ RowMap(const AttendArgs& a, int rho0) : mul(a.g_mul), g(a.g) {
+    tok0 = rho0 ? rho0 / g : 0;
+    rem0 = rho0 - tok0 * g;
+  }
+  // of row rho0 + i, i < 128: g_mul is 2^21 / g rounded up, and i + rem0 < 128 + 1024
+  __device__ __forceinline__ int token(int i) const { return tok0 + (int)((uint32_t)(i + rem0) * (uint32_t)mul >> 21); }
+  __device__ __forceinline__ int head(int i, int tok) const { return i + rem0 - (tok - tok0) * g; }
+};
+
+template <int WT, int DH, int RT, int NW>
+__global__ __launch_bounds__(64 * NW, NW == 8 || RT == 2 ? 2 : 3) void attend_split_kernel(AttendArgs a) {
   using C = AttnTile<WT, DH>;
   constexpr int KT = C::KT, NG = C::NG, NQ = C::NQ, VW = C::VW, NB = C::NB, NO = C::NO, KB = C::KB;
-  __shared__ float s_m[4][16 * RT], s_l[4][16 * RT];
-  __shared__ __attribute__((aligned(16))) float s_o[16 * RT][DH + 4];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  constexpr int TR = 16 * RT, ROW = DH * KB;
+  __shared__ float s_m[NW][TR], s_l[NW][TR];
+  __shared__ __attribute__((aligned(16))) float s_o[NW][TR][DH + 4];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int c = lane & 15, q = lane >> 4;
-  int b = blockIdx.x;
-  const int hk = b % a.h_kv;
-  b /= a.h_kv;
-  const int rtile = b % a.row_tiles;
-  b /= a.row_tiles;
-  const int split = b % a.S, r = b / a.S;
+  const int rtile = a.row_tiles == 1 ? 0 : blockIdx.x / a.h_kv, hk = blockIdx.x - rtile * a.h_kv;
+  const int split = blockIdx.y, r = blockIdx.z;
 
-  const int t0 = min(max(gp(a.cu)[r], 0), a.T), t1 = min(max(gp(a.cu)[r + 1], t0), a.T);
-  const int n = t1 - t0, g = a.g, rows = n * g;
-  const int rho0 = rtile * 16 * RT;
-  if (rho0 >= rows) return;
-  const int len = min(max(gp(a.kv_len)[r], 0), a.max_len);
-  const int past = len - n;  // position of the first new token
-  const int rho1 = min(rho0 + 16 * RT, rows) - 1;
-  // keys that some row of the tile sees
-  const int hi = max(0, min(past + rho1 / g + 1, len));
-  const int lo = a.window > 0 ? max(0, past + rho0 / g + 1 - a.window) : 0;
-  const int lo_al = lo & ~(KT - 1);
-  const int k0 = lo_al + split * a.chunk, k1 = min(k0 + a.chunk, hi);
-  if (split > 0 && k0 >= hi) return;
-  // keys that every row sees
-  const int hi_all = min(past + rho0 / g + 1, len);
-  const int lo_all = a.window > 0 ? max(0, past + rho1 / g + 1 - a.window) : 0;
-
-  const int row_bytes = DH * KB;
+  // the cache row of the first key of a group of 16, from the request's page table; a key past
+  // the sequence may name any page, of this cache
   const int lg = a.page_shift, pm = (1 << lg) - 1;
   const SFN_GLOBAL int32_t* table = gp(a.table) + (int64_t)r * a.max_pages;
-
-  // the cache row of the first key of key's group of 16
-  auto row_of = [&](int key) -> int64_t {
-    const int page = min(max(table[key >> lg], 0), a.n_pages - 1);
-    return (((int64_t)page * a.h_kv + hk) << lg) + (key & pm & ~15);
+  auto page_of = [&](int key) { return table[min(key >> lg, a.max_pages - 1)]; };
+  auto row_in = [&](int page, int key) -> int64_t {
+    return (((int64_t)min(max(page, 0), a.n_pages - 1) * a.h_kv + hk) << lg) + (key & pm & ~15);
   };
+  // without a window the first keys do not depend on the lengths: their pages are read with them
+  int page[NG];
+#pragma unroll
+  for (int u = 0; u < NG; ++u) page[u] = page_of(split * a.chunk + wave * KT + 16 * u);
+
+  const int t0 = min(max(gp(a.cu)[r], 0), a.T), t1 = min(max(gp(a.cu)[r + 1], t0), a.T);
+  const int n = t1 - t0, g = a.g, rows = min(n, a.max_new) * g;
+  const int len = min(max(gp(a.kv_len)[r], 0), a.max_len);
+  const int rho0 = rtile * TR;
+  if (rho0 >= rows) return;
+  const int past = len - n;  // position of the first new token
+  const RowMap map(a, rho0);
+  const int last = min(TR, rows - rho0) - 1, tok1 = map.token(last);
+  // keys that some row of the tile sees, and that every row sees
+  const int hi = max(0, min(past + tok1 + 1, len));
+  const int lo = a.window > 0 ? max(0, past + map.tok0 + 1 - a.window) : 0;
+  const int hi_all = min(past + map.tok0 + 1, len);
+  const int lo_all = a.window > 0 ? max(0, past + tok1 + 1 - a.window) : 0;
+  const int k0 = (lo & ~(KT - 1)) + split * a.chunk, k1 = min(k0 + a.chunk, hi);
+  if (split > 0 && k0 >= hi) return;
+
+  const int kw = k0 + wave * KT;
+  KeyTile<WT, DH> tile;
+  auto find = [&](int kt) {
+#pragma unroll
+    for (int u = 0; u < NG; ++u) page[u] = page_of(kt + 16 * u);
+  };
+  // the tile at kt, from the pages found for it, and then the pages of the one after it
+  auto fetch = [&](int kt) {
+    int64_t row[NG];
+#pragma unroll
+    for (int u = 0; u < NG; ++u) row[u] = row_in(page[u], kt + 16 * u);
+    tile.load(a, row, c, q);
+    if (kt + NW * KT < k1) find(kt + NW * KT);
+  };
+  if (kw < k1) {
+    if (lo > 0) find(kw);
+    fetch(kw);
+  }
 
   // Q: right operand, lane's row c, chunk s: values 64 s / KB + 16 q / KB ...
   uint4 qf[RT][NQ];
   int row_hi[RT], row_lo[RT];
 #pragma unroll
   for (int x = 0; x < RT; ++x) {
-    const int rho = rho0 + 16 * x + c;
-    const bool ok = rho < rows;
-    const int rr = ok ? rho : rho0;
-    const int tok = rr / g, head = hk * g + rr % g;
-    const SFN_GLOBAL char* src = gp(a.q) + (int64_t)(t0 + tok) * a.q_stride + head * row_bytes + 16 * q;
+    const bool ok = 16 * x + c <= last;
+    const int i = ok ? 16 * x + c : 0, tok = map.token(i), head = hk * g + map.head(i, tok);
+    const SFN_GLOBAL char* src = gp(a.q) + (int64_t)(t0 + tok) * a.q_stride + head * ROW + 16 * q;
 #pragma unroll
     for (int s = 0; s < NQ; ++s) qf[x][s] = ld16(src + 64 * s);
     row_hi[x] = ok ? min(past + tok + 1, len) : 0;
@@ -200,73 +328,12 @@ __global__ __launch_bounds__(256, RT == 1 ? 3 : RT == 2 ? 2 : 1) void attend_spl
     for (int o = 0; o < NO; ++o) acc[x][o] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   }
 
-  for (int kt = k0 + wave * KT; kt < k1; kt += 4 * KT) {
-    uint4 kf[NG][NQ];
-    uint32_t vf[NG][4][NB][VW * KB / 4];
-#pragma unroll
-    for (int u = 0; u < NG; ++u) {
-      const int64_t row = row_of(min(kt + 16 * u, (k1 - 1) & ~15));
-      const SFN_GLOBAL char* kp = gp(a.k) + (row + c) * row_bytes + 16 * q;
-#pragma unroll
-      for (int s = 0; s < NQ; ++s) kf[u][s] = ld16(kp + 64 * s);
-      const SFN_GLOBAL char* vp = gp(a.v) + (row + 4 * q) * row_bytes + c * VW * KB;
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-          const SFN_GLOBAL char* p = vp + j * row_bytes + nb * 16 * VW * KB;
-          if constexpr (VW * KB == 16) {
-            const uint4 w = ld16(p);
-            vf[u][j][nb][0] = w.x;
-            vf[u][j][nb][1] = w.y;
-            vf[u][j][nb][2] = w.z;
-            vf[u][j][nb][3] = w.w;
-          } else {
-            const uint64_t w = *reinterpret_cast<const SFN_GLOBAL uint64_t*>(p);
-            vf[u][j][nb][0] = (uint32_t)w;
-            vf[u][j][nb][1] = (uint32_t)(w >> 32);
-          }
-        }
-    }
-    const bool full = kt >= lo_all && kt + KT <= hi_all;  // every row sees every key of the tile
-    if (kt + KT > len) {
-#pragma unroll
-      for (int u = 0; u < NG; ++u)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-            for (int w = 0; w < VW * KB / 4; ++w)
-              vf[u][j][nb][w] = 16 * u + j < len - kt - 4 * q ? vf[u][j][nb][w] : 0u;
-    }
+  for (int kt = kw; kt < k1;) {
     // A masked key has weight 0, but 0 times a value that is not finite is NaN: a tile with a
     // masked key and such a value takes the long way below, so that no token's result
     // depends on tokens it does not see.
-    bool odd = false;
-    if (!full) {
-#pragma unroll
-      for (int u = 0; u < NG; ++u)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-            for (int w = 0; w < VW * KB / 4; ++w) odd |= not_finite<WT>(vf[u][j][nb][w]);
-      odd = __any(odd);
-      if (odd) {
-        // the finite values for all rows first; the others key by key into the rows that see
-        // them, read again
-#pragma unroll
-        for (int u = 0; u < NG; ++u)
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-              for (int w = 0; w < VW * KB / 4; ++w) vf[u][j][nb][w] = finite_part<WT>(vf[u][j][nb][w]);
-      }
-    }
+    const bool full = kt >= lo_all && kt + KT <= hi_all;  // every row sees every key of the tile
+    const bool odd = full ? false : tile.clean(len - kt, q);
 #pragma unroll
     for (int x = 0; x < RT; ++x) {
       f32x4_t s[NG];
@@ -276,10 +343,10 @@ __global__ __launch_bounds__(256, RT == 1 ? 3 : RT == 2 ? 2 : 1) void attend_spl
 #pragma unroll
         for (int i = 0; i < NQ; ++i) {
           if constexpr (C::kBf) {
-            s[u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, kf[u][i]),
+            s[u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, tile.k[u][i]),
                                                            __builtin_bit_cast(bf16x8_t, qf[x][i]), s[u], 0, 0, 0);
           } else {
-            const f32x4_t kk = __builtin_bit_cast(f32x4_t, kf[u][i]), qq = __builtin_bit_cast(f32x4_t, qf[x][i]);
+            const f32x4_t kk = __builtin_bit_cast(f32x4_t, tile.k[u][i]), qq = __builtin_bit_cast(f32x4_t, qf[x][i]);
 #pragma unroll
             for (int e = 0; e < 4; ++e) s[u] = __builtin_amdgcn_mfma_f32_16x16x4f32(kk[e], qq[e], s[u], 0, 0, 0);
           }
@@ -321,77 +388,65 @@ __global__ __launch_bounds__(256, RT == 1 ? 3 : RT == 2 ? 2 : 1) void attend_spl
           add += s[u][i];
         }
       l[x] += add;
-      add_weighted<WT, DH>(vf, s, acc[x]);
+      add_weighted<WT, DH>(tile.v, s, acc[x]);
       if (odd) {
+        // the values that are not finite: key by key, read again, into the rows that see them
 #pragma unroll 1
         for (int kk = 0; kk < KT && kt + kk < len; ++kk)
-          add_one_key<WT, DH>(gp(a.v) + (row_of(kt + kk) + (kk & 15)) * row_bytes + c * VW * KB, s, kk, q,
+          add_one_key<WT, DH>(gp(a.v) + (row_in(page_of(kt + kk), kt + kk) + (kk & 15)) * ROW + c * VW * KB, s, kk, q,
                               kt + kk < row_hi[x] && kt + kk >= row_lo[x], acc[x]);
       }
     }
+    kt += NW * KT;
+    if (kt < k1) fetch(kt);
   }
 
-  // join the four waves: a common maximum, then each adds its share in wave order
+  // join the waves: a common maximum, then the sums in wave order
 #pragma unroll
   for (int x = 0; x < RT; ++x) {
     l[x] = swap_pair_sum<16>(l[x]);
     l[x] = swap_pair_sum<32>(l[x]);
-    if (q == 0) {
-      s_m[wave][16 * x + c] = m[x];
-      s_l[wave][16 * x + c] = l[x];
-    }
+    if (q == 0) s_m[wave][16 * x + c] = m[x];
   }
   __syncthreads();
-  float w_self[RT];
+  float M[RT];
 #pragma unroll
   for (int x = 0; x < RT; ++x) {
-    const int i = 16 * x + c;
-    const float M = fmaxf(fmaxf(s_m[0][i], s_m[1][i]), fmaxf(s_m[2][i], s_m[3][i]));
-    w_self[x] = m[x] == kNegInf ? 0.f : exp2_f(m[x] - M);
+    M[x] = s_m[0][16 * x + c];
+#pragma unroll
+    for (int w = 1; w < NW; ++w) M[x] = fmaxf(M[x], s_m[w][16 * x + c]);
+    const float w_self = m[x] == kNegInf ? 0.f : exp2_f(m[x] - M[x]);
+    if (q == 0) s_l[wave][16 * x + c] = l[x] * w_self;
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < VW; e += 4)
+          *reinterpret_cast<f32x4_t*>(&s_o[wave][16 * x + c][16 * VW * nb + VW * (4 * q + i) + e]) =
+              f32x4_t{acc[x][nb * VW + e][i], acc[x][nb * VW + e + 1][i], acc[x][nb * VW + e + 2][i], acc[x][nb * VW + e + 3][i]} * w_self;
   }
-  for (int w = 0; w < 4; ++w) {
-    if (wave == w) {
-#pragma unroll
-      for (int x = 0; x < RT; ++x)
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int e = 0; e < VW; ++e) {
-              float* o = &s_o[16 * x + c][16 * VW * nb + VW * (4 * q + i) + e];
-              const float v = acc[x][nb * VW + e][i] * w_self[x];
-              *o = w == 0 ? v : *o + v;
-            }
-    }
-    __syncthreads();
-  }
-  for (int i = tid; i < 16 * RT * (DH / 4); i += 256) {
+  __syncthreads();
+  for (int i = tid; i < (last + 1) * (DH / 4); i += 64 * NW) {
     const int x = i / (DH / 4), d4 = (i % (DH / 4)) * 4;
-    const int rho = rho0 + x;
-    if (rho >= rows) continue;
-    const int tok = rho / g, head = hk * g + rho % g;
-    const float M = fmaxf(fmaxf(s_m[0][x], s_m[1][x]), fmaxf(s_m[2][x], s_m[3][x]));
+    const int tok = map.token(x), head = hk * g + map.head(x, tok);
     float L = 0.f;
+    f32x4_t o = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int w = 0; w < 4; ++w) L += s_m[w][x] == kNegInf ? 0.f : exp2_f(s_m[w][x] - M) * s_l[w][x];
-    f32x4_t o = *reinterpret_cast<const f32x4_t*>(&s_o[x][d4]);
-    const int64_t orow = (int64_t)(t0 + tok) * a.h_q + head;
+    for (int w = 0; w < NW; ++w) {
+      L += s_l[w][x];
+      o += *reinterpret_cast<const f32x4_t*>(&s_o[w][x][d4]);
+    }
     if (a.S == 1) {
-      const float inv = L == 0.f ? 0.f : 1.0f / L;
-      o *= inv;
-      if constexpr (C::kBf) {
-        *reinterpret_cast<SFN_GLOBAL uint64_t*>(gp(a.out) + (orow * DH + d4) * 2) =
-            (uint64_t)pack_bf16(o[0], o[1]) | (uint64_t)pack_bf16(o[2], o[3]) << 32;
-      } else {
-        *reinterpret_cast<SFN_GLOBAL f32x4_t*>(gp(a.out) + (orow * DH + d4) * 4) = o;
-      }
+      store_row<WT, DH>(a, t0 + tok, head, d4, o, L);
     } else {
-      const int64_t at = orow * a.S + split;
+      const int64_t at = (((int64_t)r * a.max_new + tok) * a.h_q + head) * a.S + split;
       *reinterpret_cast<SFN_GLOBAL f32x4_t*>(gp(a.part_o) + at * DH + d4) = o;
       if (d4 == 0) {
-        gp(a.part_ml)[2 * at] = M;
-        gp(a.part_ml)[2 * at + 1] = L;
+        float top = s_m[0][x];
+#pragma unroll
+        for (int w = 1; w < NW; ++w) top = fmaxf(top, s_m[w][x]);
+        *reinterpret_cast<SFN_GLOBAL f32x2_t*>(gp(a.part_ml) + 2 * at) = f32x2_t{top, L};
       }
     }
   }
@@ -593,15 +648,12 @@ __global__ __launch_bounds__(256, 2) void attend_tile_kernel(AttendArgs a) {
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   W w;
   const int c = w.c = lane & 31, h = w.h = lane >> 5;
-  int b = blockIdx.x;
-  const int hk = b % a.h_kv;
-  b /= a.h_kv;
-  const int rtile = a.row_tiles - 1 - b % a.row_tiles;  // the longest first
-  b /= a.row_tiles;
-  const int split = b % a.S, r = b / a.S;
+  const int hk = blockIdx.x % a.h_kv;
+  const int rtile = a.row_tiles - 1 - blockIdx.x / a.h_kv;  // the longest first
+  const int split = blockIdx.y, r = blockIdx.z;
 
   const int t0 = min(max(gp(a.cu)[r], 0), a.T), t1 = min(max(gp(a.cu)[r + 1], t0), a.T);
-  const int n = t1 - t0, g = a.g, rows = n * g;
+  const int n = t1 - t0, g = a.g, rows = min(n, a.max_new) * g;
   const int rho0 = rtile * kTileRows;
   if (rho0 >= rows) return;
   const int len = min(max(gp(a.kv_len)[r], 0), a.max_len);
@@ -680,7 +732,7 @@ __global__ __launch_bounds__(256, 2) void attend_tile_kernel(AttendArgs a) {
             (uint64_t)pack_bf16(w.acc[d][i] * inv, w.acc[d][i + 1] * inv) |
             (uint64_t)pack_bf16(w.acc[d][i + 2] * inv, w.acc[d][i + 3] * inv) << 32;
   } else {
-    const int64_t at = orow * a.S + split;
+    const int64_t at = (((int64_t)r * a.max_new + tok) * a.h_q + head) * a.S + split;
 #pragma unroll
     for (int d = 0; d < ND; ++d)
 #pragma unroll
@@ -694,38 +746,39 @@ __global__ __launch_bounds__(256, 2) void attend_tile_kernel(AttendArgs a) {
   }
 }
 
-// Joins the splits of one output row (a token's query head): one workgroup per row.
+// Joins the splits of one output row (a token's query head): one workgroup per row. The
+// parts lie by request and token, so that their first loads need not wait for the lengths;
+// what was never written is not used.
 template <int WT, int DH>
 __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a) {
-  const int KT = a.tile_keys, tile_rows = a.tile_rows;
   constexpr int LD = DH / 4, NS = 256 / LD;  // lanes of a row, splits side by side
-  __shared__ float s_w[256];
+  constexpr int U = 8;                       // loads in flight
+  __shared__ float s_w[kMaxSplits];
   __shared__ float s_red[8];
   __shared__ f32x4_t s_o[NS][LD];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  int b = blockIdx.x;
-  const int head = b % a.h_q;
-  b /= a.h_q;
-  const int i = b % a.max_new, r = b / a.max_new;
+  const int i = blockIdx.x, head = blockIdx.y, r = blockIdx.z;
+  const int64_t part = (((int64_t)r * a.max_new + i) * a.h_q + head) * a.S;
+  const int d4 = tid % LD, s0 = tid / LD;
+  const SFN_GLOBAL f32x4_t* src = reinterpret_cast<const SFN_GLOBAL f32x4_t*>(gp(a.part_o) + part * DH) + d4;
+  const f32x2_t ml = reinterpret_cast<const SFN_GLOBAL f32x2_t*>(gp(a.part_ml))[part + min(tid, a.S - 1)];
+  f32x4_t v[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) v[u] = src[(int64_t)min(s0 + u * NS, a.S - 1) * LD];
+
   const int t0 = min(max(gp(a.cu)[r], 0), a.T), t1 = min(max(gp(a.cu)[r + 1], t0), a.T);
   const int n = t1 - t0, g = a.g;
   if (i >= n) return;
   const int len = min(max(gp(a.kv_len)[r], 0), a.max_len), past = len - n;
-  const int rho0 = (i * g + head % g) / tile_rows * tile_rows;
-  const int rho1 = min(rho0 + tile_rows, n * g) - 1;
+  const int rho0 = (i * g + head % g) / a.tile_rows * a.tile_rows;
+  const int rho1 = min(rho0 + a.tile_rows, min(n, a.max_new) * g) - 1;
   const int hi = max(0, min(past + rho1 / g + 1, len));
   const int lo = a.window > 0 ? max(0, past + rho0 / g + 1 - a.window) : 0;
-  const int span = hi - (lo & ~(KT - 1));
-  const int used = span > 0 ? (span + a.chunk - 1) / a.chunk : 1;  // <= S <= 256
-  const int64_t orow = (int64_t)(t0 + i) * a.h_q + head;
-  float m = kNegInf, l = 0.f;
-  if (tid < used) {
-    m = gp(a.part_ml)[2 * (orow * a.S + tid)];
-    l = gp(a.part_ml)[2 * (orow * a.S + tid) + 1];
-  }
-  float M = m;
-#pragma unroll
-  for (int x = 1; x < 64; x <<= 1) M = fmaxf(M, shfl_xor_f(M, x));
+  const int span = hi - (lo & ~(a.tile_keys - 1));
+  const int used = span > 0 ? (span + a.chunk - 1) / a.chunk : 1;  // <= S <= kMaxSplits
+
+  const float m = tid < used ? ml[0] : kNegInf, l = tid < used ? ml[1] : 0.f;
+  float M = wave_max(m);
   if (lane == 0) s_red[wave] = M;
   __syncthreads();
   M = fmaxf(fmaxf(s_red[0], s_red[1]), fmaxf(s_red[2], s_red[3]));
@@ -735,73 +788,81 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a) {
   if (lane == 0) s_red[4 + wave] = L4;
   __syncthreads();
   const float L = (s_red[4] + s_red[5]) + (s_red[6] + s_red[7]);
-  const int d4 = tid % LD, s0 = tid / LD;
   f32x4_t o = {0.f, 0.f, 0.f, 0.f};
-  const SFN_GLOBAL f32x4_t* src = reinterpret_cast<const SFN_GLOBAL f32x4_t*>(gp(a.part_o) + orow * a.S * DH) + d4;
-  for (int s = s0; s < used; s += NS) {
-    const f32x4_t v = src[(int64_t)s * LD];
-    o += v * s_w[s];  // also for weight 0: NaN scores show
+  for (int s = s0; s < used; s += U * NS) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (s + u * NS < used) o += v[u] * s_w[s + u * NS];  // also for weight 0: NaN scores show
+    if (s + U * NS < used) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) v[u] = src[(int64_t)min(s + (U + u) * NS, a.S - 1) * LD];
+    }
   }
   s_o[s0][d4] = o;
   __syncthreads();
   if (tid < LD) {
     for (int s = 1; s < NS; ++s) o += s_o[s][d4];
-    o *= L == 0.f ? 0.f : 1.0f / L;
-    if constexpr (WT == WT_BF16) {
-      *reinterpret_cast<SFN_GLOBAL uint64_t*>(gp(a.out) + (orow * DH + 4 * d4) * 2) =
-          (uint64_t)pack_bf16(o[0], o[1]) | (uint64_t)pack_bf16(o[2], o[3]) << 32;
-    } else {
-      *reinterpret_cast<SFN_GLOBAL f32x4_t*>(gp(a.out) + (orow * DH + 4 * d4) * 4) = o;
-    }
+    store_row<WT, DH>(a, t0 + i, head, 4 * d4, o, L);
   }
 }
 
 template <int WT, int DH>
 void launch_sized(const AttendArgs& a, hipStream_t stream) {
-  const dim3 grid((unsigned)((int64_t)a.R * a.S * a.row_tiles * a.h_kv)), block(256);
+  // heads first: the row tiles of a key head lie a multiple of h_kv apart, so that with 8 (or
+  // 16, ...) key heads they share an XCD's L2
+  const dim3 grid(a.row_tiles * a.h_kv, a.S, a.R), block(256);
   if (a.tile_rows == kTileRows) {
     if constexpr (WT == WT_BF16) hipLaunchKernelGGL((attend_tile_kernel<DH>), grid, block, 0, stream, a);
-  } else if (a.tile_rows == 16) {
-    hipLaunchKernelGGL((attend_split_kernel<WT, DH, 1>), grid, block, 0, stream, a);
   } else {
-    hipLaunchKernelGGL((attend_split_kernel<WT, DH, 2>), grid, block, 0, stream, a);
+    const bool wide = a.S == 1;  // one workgroup for all of an item's keys: more waves
+    const dim3 threads(wide ? 512 : 256);
+    if (a.tile_rows == 16 && wide) hipLaunchKernelGGL((attend_split_kernel<WT, DH, 1, 8>), grid, threads, 0, stream, a);
+    else if (a.tile_rows == 16) hipLaunchKernelGGL((attend_split_kernel<WT, DH, 1, 4>), grid, threads, 0, stream, a);
+    else if (wide) hipLaunchKernelGGL((attend_split_kernel<WT, DH, 2, 8>), grid, threads, 0, stream, a);
+    else hipLaunchKernelGGL((attend_split_kernel<WT, DH, 2, 4>), grid, threads, 0, stream, a);
   }
   if (a.S > 1) {
-    const dim3 rows((unsigned)((int64_t)a.R * a.max_new * a.h_q));
+    const dim3 rows(a.max_new, a.h_q, a.R);
     hipLaunchKernelGGL((attend_join_kernel<WT, DH>), rows, block, 0, stream, a);
   }
 }
 
 }  // namespace
 
-// workgroups that fill the chip once: as many as are resident
-#ifndef X_SLOTS1
-#define X_SLOTS1 768
-#define X_SLOTS2 512
-#define X_SLOTST 512
-#define X_MAXS 256
-#endif
+// How the keys are split, by measurement (GPU time in a graph, bf16, heads of 128):
+//   - At least kFill workgroups, two to a compute unit: one token over 131000 keys, 64 / 8
+//     heads, takes 86 us with 512, 88 with 768 and 90 with 1024 (with fewer waves to share
+//     the memory with, each streams better, and there are fewer parts to join).
+//   - Several requests: finer, since their lengths differ and the last workgroup is waited
+//     for; splits of kLeast keys, but at most kMost workgroups. 48 requests of up to 8000 keys:
+//     147 us; with splits of 1024 keys 165, with 512 workgroups 190, with 8192 of them 152.
+//   - Up to kWhole keys: no split and no second launch. 501 keys, 32 heads: 8.8 us alone
+//     against 7.5 of two launches, which however cost the host 9.7.
+constexpr int kFill = 512, kLeast = 512, kMost = 4096, kWhole = 512;
+
 AttendPlan attend_plan(int R, int h_q, int h_kv, int dtype, int max_new, int max_len, int window) {
-  AttendPlan p;
+  AttendPlan p{};
   const int64_t rows = (int64_t)max_new * (h_q / h_kv);
   const bool bf = dtype == SFN_BF16;
   p.tile_rows = rows <= 16 ? 16 : rows <= 32 || !bf ? 32 : kTileRows;
   p.tile_keys = p.tile_rows == kTileRows ? kTileKeys : bf ? 32 : 16;
-  const int64_t tiles = (rows + p.tile_rows - 1) / p.tile_rows;
-  p.row_tiles = (int)tiles;
+  p.row_tiles = (int)((rows + p.tile_rows - 1) / p.tile_rows);
+  const int64_t base = (int64_t)R * h_kv * p.row_tiles;
+  const bool tile = p.tile_rows == kTileRows;
+  const int64_t step = tile ? kTileKeys : 4 * p.tile_keys;  // splits are multiples of it
+  auto splits = [&](int64_t span) {
+    int64_t s = (kFill + base - 1) / base;
+    if (!tile && R > 1) s = std::max<int64_t>(s, std::min<int64_t>((span + kLeast - 1) / kLeast, kMost / base));
+    return !tile && span <= kWhole ? 1 : std::min<int64_t>(s, kMaxSplits);
+  };
   // keys one row tile can span
-  int64_t span = max_len;
-  if (window > 0 && (int64_t)window + max_new + p.tile_keys < span) span = (int64_t)window + max_new + p.tile_keys;
-  if (span < 1) span = 1;
-  const int64_t base = (int64_t)R * h_kv * tiles;
-  const int64_t step = p.tile_rows == kTileRows ? p.tile_keys : 4 * p.tile_keys;  // a tile for each wave
-  const int64_t slots = p.tile_rows == 16 ? X_SLOTS1 : p.tile_rows == 32 ? X_SLOTS2 : X_SLOTST;
-  int64_t s = (slots + base - 1) / base;
-  if (s > X_MAXS) s = X_MAXS;
-  p.S_most = (int)std::min<int64_t>(s, std::max<int64_t>(1, ((int64_t)max_len + step - 1) / step));
-  const int64_t chunk = ((span + s - 1) / s + step - 1) / step * step;
+  int64_t span = std::max(1, max_len);
+  const int64_t most = std::min<int64_t>(splits(span), (span + step - 1) / step);  // with any window
+  if (window > 0) span = std::min<int64_t>(span, (int64_t)window + p.tile_rows + p.tile_keys);
+  const int64_t s = splits(span), chunk = ((span + s - 1) / s + step - 1) / step * step;
   p.chunk = (int)chunk;
   p.S = (int)((span + chunk - 1) / chunk);
+  p.parts = most > 1 ? (int64_t)R * max_new * h_q * most : 0;
   return p;
 }
 
