@@ -524,65 +524,63 @@ struct TileWave {
     }
   }
 
-  // acc += V^T P^T over the stage. With CLEAN, values that are not finite count as 0 and the
-  // return says whether there were any.
-  template <bool CLEAN>
-  __device__ __forceinline__ bool add_values(const SFN_LDS char* v, const uint32_t (&pw)[2][8]) {
+  // acc += V^T P^T over the stage
+  __device__ __forceinline__ void add_values(const SFN_LDS char* v, const uint32_t (&pw)[2][8]) {
     const int vrow = 4 * h + (c & 15) / 4, vcol = 16 * (c >> 4) + 4 * (c & 3);
-    bool odd = false;
 #pragma unroll
-    for (int d = 0; d < ND; ++d) {
-      const int col = 32 * d + vcol;
-      // 16 rows further the places repeat
-      const SFN_LDS char* at = v + vrow * ROW + v_place(vrow, col >> 3) * 16 + (col & 7) * 2;
+    for (int t = 0; t < 4; ++t) {
+      const bf16x8_t p = __builtin_bit_cast(bf16x8_t, make_uint4(pw[t >> 1][4 * (t & 1)], pw[t >> 1][4 * (t & 1) + 1],
+                                                                 pw[t >> 1][4 * (t & 1) + 2], pw[t >> 1][4 * (t & 1) + 3]));
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const bf16x8_t p = __builtin_bit_cast(bf16x8_t, make_uint4(pw[t >> 1][4 * (t & 1)], pw[t >> 1][4 * (t & 1) + 1],
-                                                                   pw[t >> 1][4 * (t & 1) + 2], pw[t >> 1][4 * (t & 1) + 3]));
-        uint2 x = read_transposed(at + 16 * t * ROW), y = read_transposed(at + (16 * t + 8) * ROW);
-        if constexpr (CLEAN) {
-          odd |= not_finite<WT_BF16>(x.x) | not_finite<WT_BF16>(x.y) | not_finite<WT_BF16>(y.x) | not_finite<WT_BF16>(y.y);
-          x = make_uint2(finite_part<WT_BF16>(x.x), finite_part<WT_BF16>(x.y));
-          y = make_uint2(finite_part<WT_BF16>(y.x), finite_part<WT_BF16>(y.y));
-        }
+      for (int d = 0; d < ND; ++d) {
+        const int col = 32 * d + vcol;
+        // 16 rows further the places repeat
+        const SFN_LDS char* at = v + vrow * ROW + v_place(vrow, col >> 3) * 16 + (col & 7) * 2;
+        const uint2 x = read_transposed(at + 16 * t * ROW), y = read_transposed(at + (16 * t + 8) * ROW);
         acc[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, make_uint4(x.x, x.y, y.x, y.y)), p, acc[d], 0, 0, 0);
       }
     }
-    return odd;
   }
 
-  // The values that are not finite, key by key, into the rows that see the key.
-  __device__ __forceinline__ void add_not_finite(const SFN_LDS char* v, const uint32_t (&pw)[2][8], int kt) {
+  // The values that are not finite, read again from the cache, key by key, into the rows that
+  // see the key. row(key): where its row of V begins.
+  template <class Row>
+  __device__ __forceinline__ void add_not_finite(Row row, const uint32_t (&pw)[2][8], int kt, int keys) {
 #pragma unroll 1
-    for (int kk = 0; kk < KT; ++kk) {
+    for (int kk = 0; kk < keys; ++kk) {
       uint32_t w = 0;  // the key's weight, in the lanes that hold it
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
         for (int i = 0; i < 16; ++i)
           w = 32 * kb + 8 * (i >> 2) + (i & 3) == kk - 4 * h ? pw[kb][i >> 1] >> (16 * (i & 1)) & 0xffffu : w;
-      int first = 4 * h;  // of the lane's values; opaque, so that no address is kept through the main loop
+      int first = 8 * h;  // of the lane's values, in bytes; opaque, so that no address is kept through the main loop
       asm("" : "+v"(first));
       const float p = __uint_as_float(__shfl((int)w, c + 32 * (kk >> 2 & 1), 64) << 16);
       const bool sees = kt + kk < row_hi && kt + kk >= row_lo;
+      const SFN_GLOBAL char* v = row(kt + kk);
 #pragma unroll
       for (int d = 0; d < ND; ++d)
 #pragma unroll
         for (int i = 0; i < 16; i += 4) {
-          const int col = 32 * d + 2 * i + first;  // the lane's values acc[d][i .. i + 3]
-          const uint64_t x4 = *reinterpret_cast<const SFN_LDS uint64_t*>(v + kk * ROW + v_place(kk, col >> 3) * 16 + (col & 7) * 2);
+          const uint64_t x4 = *reinterpret_cast<const SFN_GLOBAL uint64_t*>(v + 64 * d + 4 * i + first);  // of acc[d][i .. i + 3]
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const uint32_t x = (uint32_t)(x4 >> (16 * e)) << 16;
-            if (sees && not_finite<WT_F32>(x)) acc[d][i + e] = fmaf(p, __uint_as_float(x), acc[d][i + e]);
+            acc[d][i + e] = sees && not_finite<WT_F32>(x) ? fmaf(p, __uint_as_float(x), acc[d][i + e]) : acc[d][i + e];
           }
         }
     }
   }
 
-  // The stage's 64 keys from kt on. full: every row sees every key.
-  __device__ __forceinline__ void step(const SFN_LDS char* k, const SFN_LDS char* v, int kt, bool full,
-                                       float scale_log2) {
+  // The stage's 64 keys from kt on. full: every row sees every key. odd: values that are not
+  // finite were taken out of the stage (see add_not_finite).
+  template <class Row>
+  __device__ __forceinline__ void step(const SFN_LDS char* k, const SFN_LDS char* v, int kt, bool full, bool odd, float scale_log2,
+                                       Row row, int keys) {
+    // the matrix products first: the compute unit's other workgroup then falls out of step and
+    // does its softmax meanwhile (614 -> 589 us on the 2048-token prompts)
+    __builtin_amdgcn_s_setprio(1);
     f32x16_t s[2];
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb)
@@ -594,6 +592,7 @@ struct TileWave {
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb) s[kb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(read_frag(at + 32 * kb * ROW), q[i], s[kb], 0, 0, 0);
     }
+    __builtin_amdgcn_s_setprio(0);
     if (!full) {
       const int hi = row_hi - kt - 4 * h, lo = row_lo - kt - 4 * h;
 #pragma unroll
@@ -632,11 +631,10 @@ struct TileWave {
         pw[kb][i >> 1] = pack_bf16(p0, p1);
       }
     l += add;
-    if (full) {
-      add_values<false>(v, pw);
-    } else if (__any(add_values<true>(v, pw))) {
-      add_not_finite(v, pw, kt);
-    }
+    __builtin_amdgcn_s_setprio(1);
+    add_values(v, pw);
+    __builtin_amdgcn_s_setprio(0);
+    if (__builtin_expect(odd, 0)) add_not_finite(row, pw, kt, keys);
   }
 };
 
@@ -664,6 +662,9 @@ __global__ __launch_bounds__(256, 2) void attend_tile_kernel(AttendArgs a) {
   const int k0 = (lo & ~(KT - 1)) + split * a.chunk, k1 = min(k0 + a.chunk, hi);
   if (split > 0 && k0 >= hi) return;
 
+  // keys that every row of the tile sees
+  const int tile_hi = min(past + rho0 / g + 1, len);
+  const int tile_lo = a.window > 0 ? past + rho1 / g + 1 - a.window : 0;
   // this wave's rows
   const int w0 = rho0 + 32 * wave, w1 = min(w0 + 32, rows) - 1;  // none if w0 > w1
   const int some_hi = w0 <= w1 ? min(past + w1 / g + 1, len) : 0;  // keys that some row of it sees
@@ -694,6 +695,10 @@ __global__ __launch_bounds__(256, 2) void attend_tile_kernel(AttendArgs a) {
     const int page = min(max(table[key >> lg], 0), a.n_pages - 1);
     return ((((int64_t)page * a.h_kv + hk) << lg) + (key & pm)) * ROW;
   };
+  auto v_row = [&](int key) {
+    const int page = min(max(table[key >> lg], 0), a.n_pages - 1);
+    return gp(a.v) + ((((int64_t)page * a.h_kv + hk) << lg) + (key & pm)) * ROW;
+  };
   SFN_LDS char* const kl = (SFN_LDS char*)&s_k[0][0];
   SFN_LDS char* const vl = (SFN_LDS char*)&s_v[0][0];
   const int mine = 16 * wave * ROW;
@@ -708,15 +713,27 @@ __global__ __launch_bounds__(256, 2) void attend_tile_kernel(AttendArgs a) {
     // other buffer is free
     __builtin_amdgcn_s_waitcnt(kWaitLoads);
     __syncthreads();
-    if (kt + KT > len) {  // the last stage: what the page holds past the sequence becomes 0
-      for (int i = tid; i < (kt + KT - len) * NC; i += 256)
-        *reinterpret_cast<uint4*>(&s_v[buf ? 1 : 0][(KT - 1 - i / NC) * ROW + (i % NC) * 16]) = make_uint4(0, 0, 0, 0);
-      __syncthreads();
+    // A stage with masked keys: what the page holds past the sequence becomes 0, and so do
+    // values that are not finite (0 times one of them is NaN); those count in a way of their own
+    bool odd = false;
+    if (kt + KT > tile_hi || kt < tile_lo) {
+      for (int i = tid; i < KT * NC; i += 256) {
+        const int row = i / NC;
+        uint4* const at = reinterpret_cast<uint4*>(&s_v[buf ? 1 : 0][row * ROW + (i % NC) * 16]);
+        const uint4 x = *at;
+        if (kt + row >= len) {
+          *at = make_uint4(0, 0, 0, 0);
+        } else if (not_finite<WT_BF16>(x.x) | not_finite<WT_BF16>(x.y) | not_finite<WT_BF16>(x.z) | not_finite<WT_BF16>(x.w)) {
+          *at = make_uint4(finite_part<WT_BF16>(x.x), finite_part<WT_BF16>(x.y), finite_part<WT_BF16>(x.z), finite_part<WT_BF16>(x.w));
+          odd = true;
+        }
+      }
+      odd = __syncthreads_or(odd);
     }
     const int nx = buf ^ KT * ROW;
     if (more) W::load(gp(a.k) + at, gp(a.v) + at, kl + nx + mine, vl + nx + mine, lane);
     if (kt < some_hi && kt + KT > some_lo)
-      w.step(kl + buf, vl + buf, kt, kt >= all_lo && kt + KT <= all_hi, a.scale_log2);
+      w.step(kl + buf, vl + buf, kt, kt >= all_lo && kt + KT <= all_hi, odd, a.scale_log2, v_row, min(KT, len - kt));
   }
 
   const float l = swap_pair_sum<32>(w.l);
