@@ -509,7 +509,7 @@ int kv_cache_attend(const sfn_kv* kv, int32_t R, int32_t T, int32_t h_q, const v
     if (!aligned16(out) || !aligned4_or_null(table) || !aligned4_or_null(cu) || !aligned4_or_null(kv_len)) return SFN_EALIGN;
     if (window >= max_len) window = 0;  // every key is within it
     const sfn::AttendPlan p = sfn::attend_plan(R, h_q, kv->h_kv, kv->dtype, max_new, max_len, window);
-    if ((int64_t)R * p.S * p.row_tiles * kv->h_kv > INT32_MAX || (int64_t)R * max_new * h_q > INT32_MAX) return SFN_ESHAPE;
+    if ((int64_t)R * p.S * p.row_tiles * kv->h_kv > INT32_MAX || p.parts > INT32_MAX) return SFN_ESHAPE;
     if ((st = check_ws(ws, ws_bytes, attend_bytes(kv, p))) != SFN_OK) return st;
     sfn::AttendArgs a{};
     a.k = static_cast<const char*>(kv->k);

@@ -260,7 +260,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 || RT == 2 ? 2 : 3) void attend_sp
   // the sequence may name any page, of this cache
   const int lg = a.page_shift, pm = (1 << lg) - 1;
   const SFN_GLOBAL int32_t* table = gp(a.table) + (int64_t)r * a.max_pages;
-  auto page_of = [&](int key) { return table[min(key >> lg, a.max_pages - 1)]; };
+  auto page_of = [&](int key) { return __builtin_amdgcn_readfirstlane(table[min(key >> lg, a.max_pages - 1)]); };
   auto row_in = [&](int page, int key) -> int64_t {
     return (((int64_t)min(max(page, 0), a.n_pages - 1) * a.h_kv + hk) << lg) + (key & pm & ~15);
   };
@@ -638,41 +638,72 @@ struct TileWave {
   }
 };
 
-template <int DH>
-__global__ __launch_bounds__(256, 2) void attend_tile_kernel(AttendArgs a) {
+// KG groups of four waves: with two of them (a split of the keys for few row tiles) each takes
+// every second stage, with buffers of its own, and the groups join in LDS at the end, so that
+// there are half as many parts to write and join as with two workgroups.
+template <int DH, int KG>
+__global__ __launch_bounds__(256 * KG, 2) void attend_tile_kernel(AttendArgs a) {
   using W = TileWave<DH>;
   constexpr int ND = W::ND, NC = W::NC, ROW = W::ROW, KT = kTileKeys;
-  __shared__ __attribute__((aligned(16))) char s_k[2][KT * ROW], s_v[2][KT * ROW];
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  constexpr int STAGE = KT * ROW;  // bytes of a stage of K, and of V
+  __shared__ __attribute__((aligned(16))) char s_kv[KG * 4 * STAGE];  // a group's K stages, then its V stages
+  const int tid = threadIdx.x & 255, lane = threadIdx.x & 63;
+  const int kg = KG == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x >> 8);
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);  // in its group
   W w;
   const int c = w.c = lane & 31, h = w.h = lane >> 5;
-  const int hk = blockIdx.x % a.h_kv;
-  const int rtile = a.row_tiles - 1 - blockIdx.x / a.h_kv;  // the longest first
+  const int hk = a.row_tiles == 1 ? blockIdx.x : blockIdx.x % a.h_kv;
+  const int rtile = a.row_tiles == 1 ? 0 : a.row_tiles - 1 - blockIdx.x / a.h_kv;  // the longest first
   const int split = blockIdx.y, r = blockIdx.z;
+
+  // byte offset in the cache of this wave's 16 rows of the stage at kt (one group of keys, in
+  // one page; past the sequence any page of the cache)
+  const int lg = a.page_shift, pm = (1 << lg) - 1;
+  const SFN_GLOBAL int32_t* table = gp(a.table) + (int64_t)r * a.max_pages;
+  auto page_of = [&](int kt) { return __builtin_amdgcn_readfirstlane(table[min((kt + 16 * wave) >> lg, a.max_pages - 1)]); };
+  auto rows_in = [&](int page, int kt) -> int64_t {
+    return ((((int64_t)min(max(page, 0), a.n_pages - 1) * a.h_kv + hk) << lg) + ((kt + 16 * wave) & pm)) * ROW;
+  };
+  // without a window the first stage does not depend on the lengths: its page is read with them
+  int page = page_of(split * a.chunk + kg * KT);
 
   const int t0 = min(max(gp(a.cu)[r], 0), a.T), t1 = min(max(gp(a.cu)[r + 1], t0), a.T);
   const int n = t1 - t0, g = a.g, rows = min(n, a.max_new) * g;
+  const int len = min(max(gp(a.kv_len)[r], 0), a.max_len);
   const int rho0 = rtile * kTileRows;
   if (rho0 >= rows) return;
-  const int len = min(max(gp(a.kv_len)[r], 0), a.max_len);
   const int past = len - n;
-  const int rho1 = min(rho0 + kTileRows, rows) - 1;
-  const int hi = max(0, min(past + rho1 / g + 1, len));
-  const int lo = a.window > 0 ? max(0, past + rho0 / g + 1 - a.window) : 0;
+  const RowMap map(a, rho0);
+  const int last = min(kTileRows, rows - rho0) - 1;  // the tile's last row
+  // keys that some row of the tile sees, and that every row sees
+  const int tok1 = map.token(last);
+  const int hi = max(0, min(past + tok1 + 1, len));
+  const int lo = a.window > 0 ? max(0, past + map.tok0 + 1 - a.window) : 0;
+  const int tile_hi = min(past + map.tok0 + 1, len);
+  const int tile_lo = a.window > 0 ? past + tok1 + 1 - a.window : 0;
   const int k0 = (lo & ~(KT - 1)) + split * a.chunk, k1 = min(k0 + a.chunk, hi);
   if (split > 0 && k0 >= hi) return;
 
-  // keys that every row of the tile sees
-  const int tile_hi = min(past + rho0 / g + 1, len);
-  const int tile_lo = a.window > 0 ? past + rho1 / g + 1 - a.window : 0;
+  char* const my = s_kv + kg * 4 * STAGE;
+  SFN_LDS char* const kl = (SFN_LDS char*)my;
+  SFN_LDS char* const vl = kl + 2 * STAGE;
+  const int mine = 16 * wave * ROW;
+  const int kg0 = k0 + kg * KT;
+  if (kg0 < k1) {
+    if (lo > 0) page = page_of(kg0);
+    const int64_t at = rows_in(page, kg0);
+    W::load(gp(a.k) + at, gp(a.v) + at, kl + mine, vl + mine, lane);
+  }
+
   // this wave's rows
-  const int w0 = rho0 + 32 * wave, w1 = min(w0 + 32, rows) - 1;  // none if w0 > w1
-  const int some_hi = w0 <= w1 ? min(past + w1 / g + 1, len) : 0;  // keys that some row of it sees
-  const int some_lo = a.window > 0 ? past + w0 / g + 1 - a.window : 0;
-  const int all_hi = min(past + w0 / g + 1, len);  // and that every row sees
-  const int all_lo = a.window > 0 ? past + w1 / g + 1 - a.window : 0;
-  const bool ok = w0 + c < rows;
-  const int rho = ok ? w0 + c : rho0, tok = rho / g, head = hk * g + rho % g;
+  const int i0 = 32 * wave, i1 = min(i0 + 31, last);  // none if i0 > last
+  const int wt0 = map.token(i0), wt1 = map.token(max(i1, 0));
+  const int some_hi = i0 <= last ? min(past + wt1 + 1, len) : 0;  // keys that some row of it sees
+  const int some_lo = a.window > 0 ? past + wt0 + 1 - a.window : 0;
+  const int all_hi = min(past + wt0 + 1, len);  // and that every row sees
+  const int all_lo = a.window > 0 ? past + wt1 + 1 - a.window : 0;
+  const bool ok = i0 + c <= last;
+  const int i = ok ? i0 + c : 0, tok = map.token(i), head = hk * g + map.head(i, tok);
   w.row_hi = ok ? min(past + tok + 1, len) : 0;
   w.row_lo = a.window > 0 ? past + tok + 1 - a.window : 0;
   w.m = kNegInf;
@@ -684,31 +715,17 @@ __global__ __launch_bounds__(256, 2) void attend_tile_kernel(AttendArgs a) {
 #pragma unroll
     for (int d = 0; d < ND; ++d)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) w.acc[d][i] = 0.f;
+      for (int e = 0; e < 16; ++e) w.acc[d][e] = 0.f;
   }
-
-  const int lg = a.page_shift, pm = (1 << lg) - 1;
-  const SFN_GLOBAL int32_t* table = gp(a.table) + (int64_t)r * a.max_pages;
-  // byte offset in the cache of this wave's 16 rows of the stage at kt (one group, one page)
-  auto rows_at = [&](int kt) -> int64_t {
-    const int key = min(kt + 16 * wave, (k1 - 1) & ~15);
-    const int page = min(max(table[key >> lg], 0), a.n_pages - 1);
-    return ((((int64_t)page * a.h_kv + hk) << lg) + (key & pm)) * ROW;
-  };
   auto v_row = [&](int key) {
-    const int page = min(max(table[key >> lg], 0), a.n_pages - 1);
-    return gp(a.v) + ((((int64_t)page * a.h_kv + hk) << lg) + (key & pm)) * ROW;
+    const int p = min(max(table[key >> lg], 0), a.n_pages - 1);
+    return gp(a.v) + ((((int64_t)p * a.h_kv + hk) << lg) + (key & pm)) * ROW;
   };
-  SFN_LDS char* const kl = (SFN_LDS char*)&s_k[0][0];
-  SFN_LDS char* const vl = (SFN_LDS char*)&s_v[0][0];
-  const int mine = 16 * wave * ROW;
 
-  int64_t at = k0 < k1 ? rows_at(k0) : 0;
-  if (k0 < k1) W::load(gp(a.k) + at, gp(a.v) + at, kl + mine, vl + mine, lane);
   int buf = 0;
-  for (int kt = k0; kt < k1; kt += KT, buf ^= KT * ROW) {
-    const bool more = kt + KT < k1;
-    if (more) at = rows_at(kt + KT);
+  for (int kr = k0; kr < k1; kr += KG * KT, buf ^= STAGE) {  // a round: a stage for each group
+    const int kt = kr + kg * KT, kn = kt + KG * KT;
+    if (kn < k1) page = page_of(kn);
     // this wave's part of the stage has arrived; after the barrier everyone's has, and the
     // other buffer is free
     __builtin_amdgcn_s_waitcnt(kWaitLoads);
@@ -716,12 +733,11 @@ __global__ __launch_bounds__(256, 2) void attend_tile_kernel(AttendArgs a) {
     // A stage with masked keys: what the page holds past the sequence becomes 0, and so do
     // values that are not finite (0 times one of them is NaN); those count in a way of their own
     bool odd = false;
-    if (kt + KT > tile_hi || kt < tile_lo) {
-      for (int i = tid; i < KT * NC; i += 256) {
-        const int row = i / NC;
-        uint4* const at = reinterpret_cast<uint4*>(&s_v[buf ? 1 : 0][row * ROW + (i % NC) * 16]);
+    if (kr + KG * KT > tile_hi || kr < tile_lo) {
+      for (int e = kt < k1 ? tid : KT * NC; e < KT * NC; e += 256) {
+        uint4* const at = reinterpret_cast<uint4*>(my + 2 * STAGE + buf + e * 16);
         const uint4 x = *at;
-        if (kt + row >= len) {
+        if (kt + e / NC >= len) {
           *at = make_uint4(0, 0, 0, 0);
         } else if (not_finite<WT_BF16>(x.x) | not_finite<WT_BF16>(x.y) | not_finite<WT_BF16>(x.z) | not_finite<WT_BF16>(x.w)) {
           *at = make_uint4(finite_part<WT_BF16>(x.x), finite_part<WT_BF16>(x.y), finite_part<WT_BF16>(x.z), finite_part<WT_BF16>(x.w));
@@ -730,51 +746,96 @@ __global__ __launch_bounds__(256, 2) void attend_tile_kernel(AttendArgs a) {
       }
       odd = __syncthreads_or(odd);
     }
-    const int nx = buf ^ KT * ROW;
-    if (more) W::load(gp(a.k) + at, gp(a.v) + at, kl + nx + mine, vl + nx + mine, lane);
-    if (kt < some_hi && kt + KT > some_lo)
+    const int nx = buf ^ STAGE;
+    if (kn < k1) {
+      const int64_t at = rows_in(page, kn);
+      W::load(gp(a.k) + at, gp(a.v) + at, kl + nx + mine, vl + nx + mine, lane);
+    }
+    if (kt < min(some_hi, k1) && kt + KT > some_lo)
       w.step(kl + buf, vl + buf, kt, kt >= all_lo && kt + KT <= all_hi, odd, a.scale_log2, v_row, min(KT, len - kt));
   }
 
-  const float l = swap_pair_sum<32>(w.l);
-  if (!ok) return;
-  const int64_t orow = (int64_t)(t0 + tok) * a.h_q + head;
-  if (a.S == 1) {
-    const float inv = l == 0.f ? 0.f : 1.0f / l;
+  float l = swap_pair_sum<32>(w.l);
+  __syncthreads();  // the stages have been read: their LDS is free
+  if constexpr (KG == 2) {
+    // the second group's sums through LDS, 16 bytes a lane and step, each pair of waves in a
+    // part of its own (where the wave below then puts its rows)
+    f32x4_t* const at = reinterpret_cast<f32x4_t*>(s_kv + wave * 32 * DH * 4) + lane;
+    float* const ml = reinterpret_cast<float*>(s_kv + 128 * DH * 4) + 2 * tid;
+    if (kg == 1) {
 #pragma unroll
-    for (int d = 0; d < ND; ++d)
+      for (int d = 0; d < ND; ++d)
 #pragma unroll
-      for (int i = 0; i < 16; i += 4)
-        *reinterpret_cast<SFN_GLOBAL uint64_t*>(gp(a.out) + (orow * DH + 32 * d + 2 * i + 4 * h) * 2) =
-            (uint64_t)pack_bf16(w.acc[d][i] * inv, w.acc[d][i + 1] * inv) |
-            (uint64_t)pack_bf16(w.acc[d][i + 2] * inv, w.acc[d][i + 3] * inv) << 32;
-  } else {
-    const int64_t at = (((int64_t)r * a.max_new + tok) * a.h_q + head) * a.S + split;
-#pragma unroll
-    for (int d = 0; d < ND; ++d)
-#pragma unroll
-      for (int i = 0; i < 16; i += 4)
-        *reinterpret_cast<SFN_GLOBAL f32x4_t*>(gp(a.part_o) + at * DH + 32 * d + 2 * i + 4 * h) =
-            f32x4_t{w.acc[d][i], w.acc[d][i + 1], w.acc[d][i + 2], w.acc[d][i + 3]};
-    if (h == 0) {
-      gp(a.part_ml)[2 * at] = w.m;
-      gp(a.part_ml)[2 * at + 1] = l;
+        for (int e = 0; e < 4; ++e)
+          at[(d * 4 + e) * 64] = f32x4_t{w.acc[d][4 * e], w.acc[d][4 * e + 1], w.acc[d][4 * e + 2], w.acc[d][4 * e + 3]};
+      ml[0] = w.m;
+      ml[1] = l;
     }
+    __syncthreads();
+    if (kg == 1) return;
+    const float mo = ml[0], lo2 = ml[1];
+    const float M = fmaxf(w.m, mo);
+    const float f = w.m == kNegInf ? 0.f : exp2_f(w.m - M), fo = mo == kNegInf ? 0.f : exp2_f(mo - M);
+    w.m = M;
+    l = l * f + lo2 * fo;
+#pragma unroll
+    for (int d = 0; d < ND; ++d)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const f32x4_t o = at[(d * 4 + e) * 64];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w.acc[d][4 * e + j] = w.acc[d][4 * e + j] * f + o[j] * fo;
+      }
+  }
+  // Rows out through LDS, so that whole rows are written at once (a lane's values are 4 of
+  // every 8 of its row). 16-byte places are permuted like the stages'.
+  constexpr int OC = DH / 4;  // 16-byte places of an fp32 row
+  char* const out = s_kv + wave * 32 * DH * 4;
+  const bool whole = a.S == 1;
+  const float inv = whole ? (l == 0.f ? 0.f : 1.0f / l) : 1.f;
+#pragma unroll
+  for (int d = 0; d < ND; ++d)
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      *reinterpret_cast<f32x4_t*>(out + c * DH * 4 + (((8 * d + 2 * e + h) ^ (c & 15)) * 16)) =
+          f32x4_t{w.acc[d][4 * e], w.acc[d][4 * e + 1], w.acc[d][4 * e + 2], w.acc[d][4 * e + 3]} * inv;
+  // the lane's row in the output or in the parts, -1 if it has none
+  const int64_t orow = whole ? (int64_t)(t0 + tok) * a.h_q + head : (((int64_t)r * a.max_new + tok) * a.h_q + head) * a.S + split;
+  const int own = ok ? (int)orow : -1;
+  if (!whole && h == 0 && ok) *reinterpret_cast<SFN_GLOBAL f32x2_t*>(gp(a.part_ml) + 2 * orow) = f32x2_t{w.m, l};
+  __builtin_amdgcn_wave_barrier();
+  constexpr int RO = 64 / OC;  // rows of one step
+  const int ch = lane % OC;
+#pragma unroll
+  for (int x = 0; x < 32; x += RO) {
+    const int rr = x + lane / OC;
+    const f32x4_t v = *reinterpret_cast<const f32x4_t*>(out + rr * DH * 4 + ((ch ^ (rr & 15)) * 16));
+    const int64_t to = __shfl(own, rr, 64);
+    if (to < 0) continue;
+    if (whole)
+      *reinterpret_cast<SFN_GLOBAL uint64_t*>(gp(a.out) + (to * DH + 4 * ch) * 2) =
+          (uint64_t)pack_bf16(v[0], v[1]) | (uint64_t)pack_bf16(v[2], v[3]) << 32;
+    else
+      *reinterpret_cast<SFN_GLOBAL f32x4_t*>(gp(a.part_o) + to * DH + 4 * ch) = v;
   }
 }
 
-// Joins the splits of one output row (a token's query head): one workgroup per row. The
-// parts lie by request and token, so that their first loads need not wait for the lengths;
-// what was never written is not used.
-template <int WT, int DH>
+// Joins the splits of one output row (a token's query head): one workgroup for a row, or one
+// wave where there are rows enough to fill the chip that way and at most 64 splits. The parts
+// lie by request and token, so that their first loads need not wait for the lengths; what
+// was never written is not used.
+template <int WT, int DH, bool WAVE>
 __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a) {
-  constexpr int LD = DH / 4, NS = 256 / LD;  // lanes of a row, splits side by side
+  constexpr int NT = WAVE ? 64 : 256;        // threads of a row
+  constexpr int LD = DH / 4, NS = NT / LD;   // lanes of a row's values, splits side by side
   constexpr int U = 8;                       // loads in flight
-  __shared__ float s_w[kMaxSplits];
+  __shared__ float s_w[256];
   __shared__ float s_red[8];
-  __shared__ f32x4_t s_o[NS][LD];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int i = blockIdx.x, head = blockIdx.y, r = blockIdx.z;
+  __shared__ f32x4_t s_o[256];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, tid = WAVE ? lane : threadIdx.x;
+  const int i = blockIdx.x, r = blockIdx.z, head = WAVE ? blockIdx.y * 4 + wave : blockIdx.y;
+  if (WAVE && head >= a.h_q) return;
+  float* const w_of = s_w + (WAVE ? 64 * wave : 0);
   const int64_t part = (((int64_t)r * a.max_new + i) * a.h_q + head) * a.S;
   const int d4 = tid % LD, s0 = tid / LD;
   const SFN_GLOBAL f32x4_t* src = reinterpret_cast<const SFN_GLOBAL f32x4_t*>(gp(a.part_o) + part * DH) + d4;
@@ -784,44 +845,64 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a) {
   for (int u = 0; u < U; ++u) v[u] = src[(int64_t)min(s0 + u * NS, a.S - 1) * LD];
 
   const int t0 = min(max(gp(a.cu)[r], 0), a.T), t1 = min(max(gp(a.cu)[r + 1], t0), a.T);
-  const int n = t1 - t0, g = a.g;
+  const int n = t1 - t0;
   if (i >= n) return;
   const int len = min(max(gp(a.kv_len)[r], 0), a.max_len), past = len - n;
-  const int rho0 = (i * g + head % g) / a.tile_rows * a.tile_rows;
+  // the row tile that the row was in, and the keys that it saw
+  const int g = a.g, rho0 = (i * g + head % g) / a.tile_rows * a.tile_rows;
   const int rho1 = min(rho0 + a.tile_rows, min(n, a.max_new) * g) - 1;
   const int hi = max(0, min(past + rho1 / g + 1, len));
   const int lo = a.window > 0 ? max(0, past + rho0 / g + 1 - a.window) : 0;
   const int span = hi - (lo & ~(a.tile_keys - 1));
-  const int used = span > 0 ? (span + a.chunk - 1) / a.chunk : 1;  // <= S <= kMaxSplits
+  const int used = span > 0 ? (span + a.chunk - 1) / a.chunk : 1;  // <= S
 
   const float m = tid < used ? ml[0] : kNegInf, l = tid < used ? ml[1] : 0.f;
   float M = wave_max(m);
-  if (lane == 0) s_red[wave] = M;
-  __syncthreads();
-  M = fmaxf(fmaxf(s_red[0], s_red[1]), fmaxf(s_red[2], s_red[3]));
+  if constexpr (!WAVE) {
+    if (lane == 0) s_red[wave] = M;
+    __syncthreads();
+    M = fmaxf(fmaxf(s_red[0], s_red[1]), fmaxf(s_red[2], s_red[3]));
+  }
   const float w = m == kNegInf ? 0.f : exp2_f(m - M);
-  s_w[tid] = w;
-  const float L4 = wave_sum(w * l);
-  if (lane == 0) s_red[4 + wave] = L4;
-  __syncthreads();
-  const float L = (s_red[4] + s_red[5]) + (s_red[6] + s_red[7]);
+  w_of[tid] = w;
+  float L = wave_sum(w * l);
+  if constexpr (!WAVE) {
+    if (lane == 0) s_red[4 + wave] = L;
+    __syncthreads();
+    L = (s_red[4] + s_red[5]) + (s_red[6] + s_red[7]);
+  } else {
+    __builtin_amdgcn_wave_barrier();
+  }
   f32x4_t o = {0.f, 0.f, 0.f, 0.f};
   for (int s = s0; s < used; s += U * NS) {
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      if (s + u * NS < used) o += v[u] * s_w[s + u * NS];  // also for weight 0: NaN scores show
+      if (s + u * NS < used) o += v[u] * w_of[s + u * NS];  // also for weight 0: NaN scores show
     if (s + U * NS < used) {
 #pragma unroll
       for (int u = 0; u < U; ++u) v[u] = src[(int64_t)min(s + (U + u) * NS, a.S - 1) * LD];
     }
   }
-  s_o[s0][d4] = o;
-  __syncthreads();
+  f32x4_t* const o_of = s_o + (WAVE ? 64 * wave : 0);
+  o_of[tid] = o;
+  if constexpr (WAVE) __builtin_amdgcn_wave_barrier();
+  else __syncthreads();
   if (tid < LD) {
-    for (int s = 1; s < NS; ++s) o += s_o[s][d4];
+#pragma unroll
+    for (int s = 1; s < NS; ++s) o += o_of[s * LD + d4];
     store_row<WT, DH>(a, t0 + i, head, 4 * d4, o, L);
   }
 }
+
+// Tile kernel: up to this many workgroups get two groups of waves (one to a compute unit),
+// and few row tiles are split into about as many. The 16-token chunk of four requests, 64 / 8
+// heads, up to 6000 keys: 28.7 us, with 384 or 512 splits 41 and 40 (before a row's parts were
+// joined by one wave).
+constexpr int kTileFill = 256;
+// From so many rows on a wave joins one instead of a workgroup: 28.7 against 31.8 us there,
+// 10.1 against 11.2 us for the 888 rows of an fp32 chunk, but 91.5 against 89.8 us for 64 rows
+// of 64 splits.
+constexpr int kJoinByWave = 512;
 
 template <int WT, int DH>
 void launch_sized(const AttendArgs& a, hipStream_t stream) {
@@ -829,7 +910,11 @@ void launch_sized(const AttendArgs& a, hipStream_t stream) {
   // 16, ...) key heads they share an XCD's L2
   const dim3 grid(a.row_tiles * a.h_kv, a.S, a.R), block(256);
   if (a.tile_rows == kTileRows) {
-    if constexpr (WT == WT_BF16) hipLaunchKernelGGL((attend_tile_kernel<DH>), grid, block, 0, stream, a);
+    if constexpr (WT == WT_BF16) {
+      if ((int64_t)a.R * a.S * a.row_tiles * a.h_kv > kTileFill)
+        hipLaunchKernelGGL((attend_tile_kernel<DH, 1>), grid, block, 0, stream, a);
+      else hipLaunchKernelGGL((attend_tile_kernel<DH, 2>), grid, dim3(512), 0, stream, a);
+    }
   } else {
     const bool wide = a.S == 1;  // one workgroup for all of an item's keys: more waves
     const dim3 threads(wide ? 512 : 256);
@@ -839,8 +924,10 @@ void launch_sized(const AttendArgs& a, hipStream_t stream) {
     else hipLaunchKernelGGL((attend_split_kernel<WT, DH, 2, 4>), grid, threads, 0, stream, a);
   }
   if (a.S > 1) {
-    const dim3 rows(a.max_new, a.h_q, a.R);
-    hipLaunchKernelGGL((attend_join_kernel<WT, DH>), rows, block, 0, stream, a);
+    if (a.S <= 64 && (int64_t)a.R * a.max_new * a.h_q >= kJoinByWave)
+      hipLaunchKernelGGL((attend_join_kernel<WT, DH, true>), dim3(a.max_new, (a.h_q + 3) / 4, a.R), dim3(256), 0, stream, a);
+    else
+      hipLaunchKernelGGL((attend_join_kernel<WT, DH, false>), dim3(a.max_new, a.h_q, a.R), dim3(256), 0, stream, a);
   }
 }
 
@@ -856,7 +943,6 @@ void launch_sized(const AttendArgs& a, hipStream_t stream) {
 //   - Up to kWhole keys: no split and no second launch. 501 keys, 32 heads: 8.8 us alone
 //     against 7.5 of two launches, which however cost the host 9.7.
 constexpr int kFill = 512, kLeast = 512, kMost = 4096, kWhole = 512;
-
 AttendPlan attend_plan(int R, int h_q, int h_kv, int dtype, int max_new, int max_len, int window) {
   AttendPlan p{};
   const int64_t rows = (int64_t)max_new * (h_q / h_kv);
@@ -868,7 +954,7 @@ AttendPlan attend_plan(int R, int h_q, int h_kv, int dtype, int max_new, int max
   const bool tile = p.tile_rows == kTileRows;
   const int64_t step = tile ? kTileKeys : 4 * p.tile_keys;  // splits are multiples of it
   auto splits = [&](int64_t span) {
-    int64_t s = (kFill + base - 1) / base;
+    int64_t s = tile ? std::max<int64_t>(1, kTileFill / base) : (kFill + base - 1) / base;
     if (!tile && R > 1) s = std::max<int64_t>(s, std::min<int64_t>((span + kLeast - 1) / kLeast, kMost / base));
     return !tile && span <= kWhole ? 1 : std::min<int64_t>(s, kMaxSplits);
   };
