@@ -125,6 +125,15 @@ _lib.residual_norm.argtypes = [ctypes.POINTER(sfn_norm), _i32, _vp, _i32, _vp, _
 _lib.residual_norm.restype = ctypes.c_int
 
 
+# the tensor checks of the paged cache's calls and the norm, compiled (csrc/torch_args.cpp)
+try:
+    from . import _torch_args as _args
+except ImportError as e:
+    raise ImportError(f"{e}: build it with `python -m contextual_activation_sparsity_amd.build`") from e
+_args.bind(*(ctypes.cast(f, ctypes.c_void_p).value
+             for f in (_lib.kv_cache_plan, _lib.kv_cache_append, _lib.kv_cache_attend, _lib.residual_norm)))
+
+
 class SparseFFNError(RuntimeError):
     def __init__(self, status, call):
         self.status = status
@@ -339,6 +348,7 @@ class KVCache:
         self.dtype = self.k.dtype
         self.c = sfn_kv(self.n_pages, self.page, self.h_kv, self.dh, _WDT[self.dtype], 0, _ptr(self.k, "k"),
                         _ptr(self.v, "v"))
+        self.addr = ctypes.addressof(self.c)
 
 
 @dataclass
@@ -359,55 +369,21 @@ class ResidualNorm:
             raise ValueError(f"w_post must be [{self.d}]")
         self.c = sfn_norm(self.d, _WDT[self.dtype], float(self.eps), float(self.scale),
                           _ptr(self.w_post, "w_post", self.dtype), _ptr(self.w_pre, "w_pre"))
-
-
-def _token_rows(t: torch.Tensor, name, dtype, heads, dh):
-    """Address and token stride (elements) of [T, heads, dh] rows, or of parts of wider rows."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a GPU tensor (got {t.device})")
-    if t.dtype is not dtype:
-        raise ValueError(f"{name} must be {dtype} (got {t.dtype})")
-    n, h, w = t.shape
-    s0, s1, s2 = t.stride()
-    if w != dh or (heads is not None and h != heads):
-        raise ValueError(f"{name} must be [T, {'heads' if heads is None else heads}, {dh}] (got {tuple(t.shape)})")
-    if s2 != 1 or (s1 != dh and h > 1):
-        raise ValueError(f"{name}: the heads of a token must lie one after the other")
-    return t.data_ptr(), (s0 if n > 1 else h * dh)
+        self.addr = ctypes.addressof(self.c)
 
 
 def kv_cache_plan(kv: KVCache, held_len: torch.Tensor, ctx_len: torch.Tensor, new_len: torch.Tensor, table: torch.Tensor,
                   free_pages: torch.Tensor, n_free: torch.Tensor, n_free_out: torch.Tensor, cu: torch.Tensor,
                   kv_len: torch.Tensor, pos: torch.Tensor, slot: torch.Tensor, status: torch.Tensor, stream=None):
-    i32, R = torch.int32, held_len.numel()
-    if table.dim() != 2 or table.shape[0] != R:
-        raise ValueError(f"table must be [{R}, max_pages]")
-    T = slot.numel()
-    st = _lib.kv_cache_plan(
-        kv.c, R, table.shape[1], T, _ptr(held_len, "held_len", i32), _ptr(ctx_len, "ctx_len", i32, R),
-        _ptr(new_len, "new_len", i32, R), _ptr(table, "table", i32), _ptr(free_pages, "free_pages", i32, kv.n_pages),
-        _ptr(n_free, "n_free", i32, 1), _ptr(n_free_out, "n_free_out", i32, 1), _ptr(cu, "cu", i32, R + 1),
-        _ptr(kv_len, "kv_len", i32, R), _ptr(pos, "pos", i32, T), _ptr(slot, "slot", i32), _ptr(status, "status", i32, 1),
-        _stream(stream))
+    st = _args.plan(kv.addr, held_len, ctx_len, new_len, table, free_pages, n_free, n_free_out, cu, kv_len, pos, slot,
+                    status, _stream(stream))
     _check(st, "kv_cache_plan")
 
 
 def kv_cache_append(kv: KVCache, k: torch.Tensor, v: torch.Tensor, slot: torch.Tensor, q: Optional[torch.Tensor] = None,
                     q_out: Optional[torch.Tensor] = None, pos: Optional[torch.Tensor] = None,
                     rope: Optional[torch.Tensor] = None, stream=None):
-    T = k.shape[0]
-    if v.shape[0] != T or (q is not None and q.shape[0] != T):
-        raise ValueError("q, k and v must hold the same tokens")
-    kp, ks = _token_rows(k, "k", kv.dtype, kv.h_kv, kv.dh)
-    vp, vs = _token_rows(v, "v", kv.dtype, kv.h_kv, kv.dh)
-    qp, qs, h_q = None, 0, 0
-    if q is not None:
-        h_q = q.shape[1]
-        qp, qs = _token_rows(q, "q", kv.dtype, h_q, kv.dh)
-    n_pos, rot = (0, 0) if rope is None else rope.shape
-    st = _lib.kv_cache_append(
-        kv.c, T, h_q, qp, qs, kp, ks, vp, vs, _ptr(pos, "pos", torch.int32, T), _ptr(slot, "slot", torch.int32, T),
-        _ptr(rope, "rope", torch.float32), n_pos, rot, _ptr(q_out, "q_out", kv.dtype, T * h_q * kv.dh), _stream(stream))
+    st = _args.append(kv.addr, k, v, slot, q, q_out, pos, rope, _stream(stream))
     _check(st, "kv_cache_append")
 
 
@@ -418,30 +394,14 @@ def kv_cache_attend_workspace_size(kv: KVCache, R: int, T: int, h_q: int, max_ne
 def kv_cache_attend(kv: KVCache, q: torch.Tensor, table: torch.Tensor, cu: torch.Tensor, kv_len: torch.Tensor,
                     out: torch.Tensor, ws: torch.Tensor, max_new: int, max_len: int, scale: Optional[float] = None,
                     window: int = 0, stream=None):
-    i32 = torch.int32
-    T, h_q, _ = q.shape
-    R, max_pages = table.shape
-    qp, qs = _token_rows(q, "q", kv.dtype, h_q, kv.dh)
-    st = _lib.kv_cache_attend(
-        kv.c, R, T, h_q, qp, qs, _ptr(table, "table", i32), max_pages, _ptr(cu, "cu", i32, R + 1),
-        _ptr(kv_len, "kv_len", i32, R), max_new, max_len, kv.dh ** -0.5 if scale is None else scale, window,
-        _ptr(out, "out", kv.dtype, T * h_q * kv.dh), _ptr(ws, "ws"), ws.numel() * ws.element_size(), _stream(stream))
+    st = _args.attend(kv.addr, q, table, cu, kv_len, out, ws, max_new, max_len, kv.dh ** -0.5 if scale is None else scale,
+                      window, _stream(stream))
     _check(st, "kv_cache_attend")
 
 
 def residual_norm(norm: ResidualNorm, h: torch.Tensor, y: Optional[torch.Tensor], h_out: Optional[torch.Tensor],
                   x_out: Optional[torch.Tensor], gate: Optional[torch.Tensor] = None, stream=None):
-    d = norm.d
-    if h.dtype not in _WDT or (y is not None and y.dtype not in _WDT):
-        raise ValueError("h and y must be bfloat16 or float32")
-    T = h.numel() // d
-    if h.numel() != T * d:
-        raise ValueError(f"h must be [T, {d}]")
-    stride = 0 if gate is None or gate.numel() == d and gate.dim() == 1 else d
-    st = _lib.residual_norm(
-        norm.c, T, _ptr(h, "h"), _WDT[h.dtype], _ptr(y, "y", None, T * d), SFN_F32 if y is None else _WDT[y.dtype],
-        _ptr(gate, "gate", norm.dtype, T * d if stride else d), stride, _ptr(h_out, "h_out", h.dtype, T * d),
-        _ptr(x_out, "x_out", norm.dtype, T * d), _stream(stream))
+    st = _args.norm(norm.addr, h, y, h_out, x_out, gate, _stream(stream))
     _check(st, "residual_norm")
 
 

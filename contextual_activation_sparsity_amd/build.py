@@ -4,7 +4,8 @@
 
 Each source is compiled to an object in ``_build/`` (in parallel), then linked into
 ``contextual_activation_sparsity_amd/libsparse_ffn.so`` next to the binding that loads
-it. Compiles every time it is called. hipcc cross-compiles, so no GPU is needed.
+it, and ``csrc/torch_args.cpp`` (the binding's compiled tensor checks) into
+``_torch_args.so`` beside it. Compiles every time it is called. hipcc cross-compiles, so no GPU is needed.
 
 ``--sanitize`` instead builds ``_build/san/libsparse_ffn_san.so`` with AddressSanitizer
 and UndefinedBehaviorSanitizer on the host code only (device code is built as usual).
@@ -23,6 +24,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -30,6 +32,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libsparse_ffn.so")
+ARGS_LIB = os.path.join(PKG, "_torch_args.so")
 SAN_BUILD = os.path.join(BUILD, "san")
 SAN_LIB = os.path.join(SAN_BUILD, "libsparse_ffn_san.so")
 
@@ -89,7 +92,29 @@ def build(jobs=None, verbose=False, sanitize=False):
     if res.returncode != 0:
         raise RuntimeError(f"link failed:\n{res.stderr}")
     os.replace(tmp, lib)
+    if not sanitize:
+        build_args(verbose)
     return lib
+
+
+def build_args(verbose=False):
+    """The binding's tensor checks, a host-only extension module against torch's headers."""
+    import torch
+    from torch.utils.cpp_extension import include_paths
+
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    inc = [f"-I{p}" for p in (INCLUDE, sysconfig.get_paths()["include"], *include_paths())]
+    tmp = ARGS_LIB + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *inc, os.path.join(CSRC, "torch_args.cpp"), "-o", tmp, f"-L{lib}", "-ltorch_python", "-ltorch_cpu", "-lc10",
+           f"-Wl,-rpath,{lib}"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"compile of torch_args.cpp failed:\n{res.stderr}")
+    os.replace(tmp, ARGS_LIB)
+    return ARGS_LIB
 
 
 def main(argv=None):
