@@ -429,7 +429,12 @@ int kv_cache_plan(const sfn_kv* kv, int32_t R, int32_t max_pages, int32_t max_to
       if (!p) return SFN_EINVAL;
       if (!aligned4_or_null(p)) return SFN_EALIGN;
     }
-    if (n_free == n_free_out) return SFN_EINVAL;
+    // outputs that are read as inputs while they are written
+    const void* in[] = {held_len, ctx_len, new_len, n_free};
+    const void* out[] = {table, free_pages, n_free_out, cu, kv_len, pos, slot, status};
+    for (const void* i : in)
+      for (const void* o : out)
+        if (i == o) return SFN_EINVAL;
     sfn::KvPlanArgs a{held_len, ctx_len, new_len, table, free_pages, n_free, n_free_out, cu, kv_len, pos, slot, status,
                       R, max_pages, max_tokens, kv->n_pages, page_shift(kv->page)};
     return hip_status(sfn::launch_kv_plan(a, static_cast<hipStream_t>(stream)));

@@ -100,6 +100,7 @@ struct KvPlanArgs {
   const int32_t* n_free;
   int32_t *n_free_out, *cu, *kv_len, *pos, *slot, *status;
   int R, max_pages, max_tokens, n_pages, page_shift;
+  int token_groups;  // workgroups that place tokens (set by the launch)
 };
 hipError_t launch_kv_plan(const KvPlanArgs& a, hipStream_t stream);
 

@@ -940,9 +940,10 @@ void launch_sized(const AttendArgs& a, hipStream_t stream) {
 //   - Several requests: finer, since their lengths differ and the last workgroup is waited
 //     for; splits of kLeast keys, but at most kMost workgroups. 48 requests of up to 8000 keys:
 //     147 us; with splits of 1024 keys 165, with 512 workgroups 190, with 8192 of them 152.
-//   - Up to kWhole keys: no split and no second launch. 501 keys, 32 heads: 8.8 us alone
-//     against 7.5 of two launches, which however cost the host 9.7.
-constexpr int kFill = 512, kLeast = 512, kMost = 4096, kWhole = 512;
+//   - Up to kWhole keys: no split and no second launch. 32 / 32 heads, each call from Python:
+//     201 keys 5.7 us against 7.7 in two launches, 301 keys 7.2 against 7.7, but 501 keys 10.5
+//     against 8.3 (one compute unit's load rate bounds an unsplit item).
+constexpr int kFill = 512, kLeast = 512, kMost = 4096, kWhole = 384;
 AttendPlan attend_plan(int R, int h_q, int h_kv, int dtype, int max_new, int max_len, int window) {
   AttendPlan p{};
   const int64_t rows = (int64_t)max_new * (h_q / h_kv);

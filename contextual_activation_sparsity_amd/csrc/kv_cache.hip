@@ -50,6 +50,7 @@ __global__ __launch_bounds__(kPlanThreads) void kv_plan_kernel(KvPlanArgs a) {
   int* const s_rel = s_cu + 2 * (R + 1);
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   if (tid == 0) s_bad = 0;
+  const int n_free = min(max(gp(a.n_free)[0], 0), a.n_pages);
   __syncthreads();
   const int per = (R + kPlanThreads - 1) / kPlanThreads;
   const int r0 = tid * per, r1 = min(R, r0 + per);
@@ -95,11 +96,14 @@ __global__ __launch_bounds__(kPlanThreads) void kv_plan_kernel(KvPlanArgs a) {
   }
   __syncthreads();
   const int T = s_new[R], takes = s_take[R], rels = s_rel[R];
-  const int n_free = min(max(gp(a.n_free)[0], 0), a.n_pages);
   const int short_by = takes - rels - n_free;
   const int status = (s_bad || T > a.max_tokens || n_free + rels > a.n_pages) ? -1 : short_by > 0 ? short_by : 0;
   const bool ok = status == 0;
-  const int gid = blockIdx.x * kPlanThreads + tid, gsz = gridDim.x * kPlanThreads;
+  // the first workgroups place the tokens, the others everything that goes by request or page:
+  // each is a chain of dependent reads, and the chains run side by side
+  const bool tokens = (int)blockIdx.x < a.token_groups;
+  const int gid = (tokens ? blockIdx.x : blockIdx.x - a.token_groups) * kPlanThreads + tid;
+  const int gsz = (tokens ? a.token_groups : gridDim.x - a.token_groups) * kPlanThreads;
 
   auto released = [&](int i) {  // number i of the pages given back
     const int r = upper(s_rel, R, i);
@@ -110,17 +114,20 @@ __global__ __launch_bounds__(kPlanThreads) void kv_plan_kernel(KvPlanArgs a) {
     const int top = n_free + rels - 1 - j;
     return top >= n_free ? released(top - n_free) : gp(a.free_pages)[top];
   };
-  for (int t = gid; t < a.max_tokens; t += gsz) {
-    int pos = 0, slot = -1;
-    if (ok && t < T) {
-      const int r = upper(s_new, R, t);
-      pos = gp(a.ctx)[r] + t - s_new[r];
-      const int e = pos >> lg, h = (gp(a.held)[r] + pm) >> lg;
-      const int page = e < h ? gp(a.table)[(int64_t)r * a.max_pages + e] : taken(s_take[r] + e - h);
-      slot = (page << lg) + (pos & pm);
+  if (tokens) {
+    for (int t = gid; t < a.max_tokens; t += gsz) {
+      int pos = 0, slot = -1;
+      if (ok && t < T) {
+        const int r = upper(s_new, R, t);
+        pos = gp(a.ctx)[r] + t - s_new[r];
+        const int e = pos >> lg, h = (gp(a.held)[r] + pm) >> lg;
+        const int page = e < h ? gp(a.table)[(int64_t)r * a.max_pages + e] : taken(s_take[r] + e - h);
+        slot = (page << lg) + (pos & pm);
+      }
+      gp(a.pos)[t] = pos;
+      gp(a.slot)[t] = slot;
     }
-    gp(a.pos)[t] = pos;
-    gp(a.slot)[t] = slot;
+    return;
   }
   for (int r = gid; r < R; r += gsz) {
     gp(a.kv_len)[r] = ok ? gp(a.ctx)[r] + gp(a.fresh)[r] : 0;
@@ -248,11 +255,13 @@ __global__ __launch_bounds__(256) void kv_append_kernel(KvAppendArgs a) {
 }  // namespace
 
 hipError_t launch_kv_plan(const KvPlanArgs& a, hipStream_t stream) {
-  // a workgroup for every 512 tokens or requests; more than 256 would only repeat the sums
-  const int most = a.max_tokens > a.R ? a.max_tokens : a.R;
-  int g = (most + kPlanThreads - 1) / kPlanThreads;
-  if (g > 256) g = 256;
-  hipLaunchKernelGGL(kv_plan_kernel, dim3(g), dim3(kPlanThreads), 3 * (a.R + 1) * sizeof(int), stream, a);
+  // a workgroup for every 512 tokens (more than 200 would only repeat the sums), and two for
+  // every 512 requests, which take or give back a page each now and then
+  KvPlanArgs b = a;
+  b.token_groups = (a.max_tokens + kPlanThreads - 1) / kPlanThreads;
+  if (b.token_groups > 200) b.token_groups = 200;
+  const int g = b.token_groups + 2 * ((a.R + kPlanThreads - 1) / kPlanThreads);
+  hipLaunchKernelGGL(kv_plan_kernel, dim3(g), dim3(kPlanThreads), 3 * (a.R + 1) * sizeof(int), stream, b);
   return hipGetLastError();
 }
 

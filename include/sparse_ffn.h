@@ -321,7 +321,7 @@ typedef struct sfn_kv {
  *   table      [R, max_pages]: in, the held pages; out, with the taken pages written;
  *              entries past the needed ones are not cleared
  *   free_pages [n_pages]: the stack, its first *n_free entries free; pushed pages written
- *   n_free     1 int32, read;  n_free_out  1 int32, written (not the same address)
+ *   n_free     1 int32, read;  n_free_out  1 int32, written
  *   cu         [R + 1], kv_len [R] (ctx_len + new_len), written
  *   pos, slot  [max_tokens], written: past the last token 0 and -1
  *   status     1 int32, written: 0; the number of pages missing; or -1 for lengths that
@@ -329,7 +329,8 @@ typedef struct sfn_kv {
  *              tokens, or a stack that would outgrow n_pages. Unless 0 nothing is taken or
  *              given back (table and stack unchanged, *n_free_out = *n_free), cu and kv_len
  *              are 0 and every slot -1, so the calls after it write and attend to nothing.
- * Planning the same inputs again gives the same result. R <= 4096, max_tokens <= 262144.
+ * Outputs must not overlap inputs. Planning the same inputs again gives the same result.
+ * R <= 4096, max_tokens <= 262144.
  */
 int kv_cache_plan(const sfn_kv* kv, int32_t R, int32_t max_pages, int32_t max_tokens, const int32_t* held_len,
                   const int32_t* ctx_len, const int32_t* new_len, int32_t* table, int32_t* free_pages,
