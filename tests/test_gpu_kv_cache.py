@@ -402,3 +402,67 @@ def test_steps_with_rollback_match_a_dense_cache(graphed):
         held = [c + x for c, x in zip(ctx, new)]
         used = sum(-(-h // page) for h in held)
         assert st["n"].item() == n_pages - used
+
+
+# ---- every kernel variant ------------------------------------------------------------
+
+
+@pytest.mark.parametrize("dh", [64, 128])
+@pytest.mark.parametrize("window", [0, 130])
+def test_attend_prompts_that_fill_the_chip(dh, window):
+    """More than 256 row tiles of 128: one group of waves to a workgroup, no splits."""
+    check_attend(BF, 16, 16, dh, 32, [(700, 650), (640, 640), (300, 129), (650, 650)], window=window, seed=20)
+
+
+def test_attend_infinities_among_many_row_tiles():
+    lens, cu = [650, 640], [0, 650, 1290]
+    k, v, table = random_cache(lens, 32, 64, 64, BF, 21)
+    q = torch.randn((1290, 32, 64), generator=torch.Generator().manual_seed(22)).to(BF)
+    say("[attend] infinities among many row tiles")
+    clean = run_attend(q, k, v, table, cu, lens)
+    p = 300  # of the first request
+    page, off = int(table[0, p // 64]), p % 64
+    v[page, 5, off, 9] = float("inf")
+    out = run_attend(q, k, v, table, cu, lens)
+    same = torch.ones(out.shape, dtype=torch.bool, device="cuda")
+    same[p:650, 5, 9] = False
+    assert torch.equal(out[same], clean[same]) and (out[~same] == float("inf")).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("n", [4, 16])
+def test_attend_many_rows_with_splits(dtype, n):
+    """Enough rows that a wave joins each, and several splits to join."""
+    check_attend(dtype, 8, 2, 128, 64, [(2100, n), (1500, n), (60, n), (900, n)] * (4 if n == 4 else 1) + [(800, n)], seed=23)
+    check_attend(dtype, 16, 4, 64, 16, [(1300, n), (1, 1), (777, n), (0, 0), (1024, n)], seed=24, window=900)
+
+
+def test_attend_bounds_that_are_too_small():
+    """Tokens past max_new are not computed (and not written), keys past max_len not read."""
+    lens, cu = [90, 200], [0, 40, 60]
+    for dtype, max_new in ((BF, 3), (F32, 9), (BF, 17)):
+        k, v, table = random_cache(lens, 2, 128, 16, dtype, 25)
+        q = torch.randn((60, 4, 128), generator=torch.Generator().manual_seed(26)).to(dtype)
+        say(f"[attend] max_new {max_new} of 40 and 20, {dtype}")
+        out = run_attend(q, k, v, table, cu, lens, max_new=max_new)
+        for sl, want, bound in attend_oracle(q, k, v, table, cu, lens, 0, 128 ** -0.5):
+            within(out[sl][:max_new], want[:max_new], bound[:max_new], "computed tokens")
+            assert torch.isnan(out[sl][max_new:]).all()
+    out = run_attend(q, k, v, table, cu, lens, max_len=100)
+    cut = [90, 100]
+    for sl, want, bound in attend_oracle(q, k, v, table, cu, cut, 0, 128 ** -0.5):
+        within(out[sl], want, bound, "cut at 100 keys")
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_attend_drawn(seed):
+    rng = random.Random(seed)
+    h_q, h_kv = rng.choice([(4, 4), (8, 2), (7, 1), (28, 4), (16, 1), (12, 4), (3, 3)])
+    reqs = []
+    for _ in range(rng.randint(1, 9)):
+        n = rng.choice([0, 1, 1, rng.randint(1, 16), rng.randint(1, 150)])
+        reqs.append((n + rng.choice([0, rng.randint(0, 40), rng.randint(0, 1500)]), n))
+    if not sum(n for _, n in reqs):
+        reqs.append((17, 1))
+    check_attend(rng.choice([BF, BF, F32]), h_q, h_kv, rng.choice([64, 128]), rng.choice([16, 32, 64, 128, 256]), reqs,
+                 window=rng.choice([0, 0, rng.randint(1, 600)]), seed=seed, strided=rng.random() < 0.3)
