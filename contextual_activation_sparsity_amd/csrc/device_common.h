@@ -125,14 +125,6 @@ __device__ __forceinline__ float swap_pair_sum(float v) {
   return a + b;
 }
 
-// The larger of v and the v of lane l ^ BIT (BIT 16 or 32), the same in both lanes.
-template <int BIT>
-__device__ __forceinline__ float swap_pair_max(float v) {
-  float a = v, b = v;
-  lane_swap<BIT>(a, b);
-  return fmaxf(a, b);
-}
-
 // Sum over each aligned group of N consecutive lanes (N a power of two, at most 64);
 // every lane of a group receives its total. Each step adds a partner lane that lies in
 // the other half of the current group (a mirror or a swap; which lane of that half does
@@ -235,16 +227,6 @@ template <int V>
 __device__ __forceinline__ void wave_transpose_sum(float* s) {
   static_assert(V <= 16, "reduce larger sets in blocks of 16");
   transpose_sum_rec<V, 32>(s);
-}
-
-// 2^x by the hardware's exponential (one instruction; results below the smallest normal
-// number flush to zero, which for softmax weights relative to the row's largest is nothing).
-__device__ __forceinline__ float exp2_f(float x) { return __builtin_amdgcn_exp2f(x); }
-
-// Two fp32 values rounded to bf16 (nearest, ties to even; NaN stays NaN), a in the low half.
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-  typedef __attribute__((ext_vector_type(2))) float f32x2_t;
-  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_t{a, b}), bf16x2_t));
 }
 
 __device__ __forceinline__ float silu_f(float g) { return g / (1.0f + __expf(-g)); }

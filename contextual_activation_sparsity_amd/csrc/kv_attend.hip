@@ -1,10 +1,9 @@
 // Attention of each request's new tokens over its pages of the key/value cache.
 
 #include <algorithm>
-#include <type_traits>
 
-#include "device_common.h"
 #include "kernels.h"
+#include "serving_common.h"
 #include "sparse_ffn.h"
 
 namespace sfn {

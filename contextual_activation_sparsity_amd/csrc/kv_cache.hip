@@ -1,8 +1,8 @@
 // The paged key/value cache's bookkeeping and writes: the plan of a step (which pages each
 // request holds, where each new token goes) and the append of the step's keys and values.
 
-#include "device_common.h"
 #include "kernels.h"
+#include "serving_common.h"
 #include "sparse_ffn.h"
 
 namespace sfn {

@@ -6,8 +6,8 @@
 // output is rounded once. HBM bound for many tokens; for one token, the launch, one round
 // of loads and two workgroup-wide sums.
 
-#include "device_common.h"
 #include "kernels.h"
+#include "serving_common.h"
 #include "sparse_ffn.h"
 
 namespace sfn {
