@@ -17,12 +17,15 @@ constexpr int kMaxSplits = 256;  // the join kernel's threads
 
 // ---- split attention -----------------------------------------------------------------
 //
-// A workgroup takes 16 RT rows of one key head's queries (row rho of a request is its
-// token rho / g, head rho % g of the g query heads that share the key head, so grouped
-// heads fill the matrix tile) and one split of the keys; its four waves take every fourth
-// tile of the split, each with a softmax of its own (running maximum and sum, fp32), and
-// join at the end. K, Q, P and V go from memory to the matrix cores through registers
-// alone. The scores are computed as S^T = K Q^T, whose tile leaves one query row per lane
+// For few query rows to a key head (up to 32), and for fp32. A workgroup takes 16 RT rows of
+// one key head's queries (row rho of a request is its token rho / g, head rho % g of the g
+// query heads that share the key head, so grouped heads fill the matrix tile) and one split
+// of the keys; its NW waves take every NW-th tile of the split, each with a softmax of its
+// own (running maximum and sum, fp32), and join at the end. K, Q, P and V go from memory to
+// the matrix cores through registers alone: at these sizes the products are far from their
+// bound, and streaming through LDS (as the tile kernel does) took 102 us where this takes
+// 83. Nor do registers for two tiles at once help (105 against 93 us with 8 waves): twelve
+// waves of 16 KB each already keep more than enough bytes under way. The scores are computed as S^T = K Q^T, whose tile leaves one query row per lane
 // (lane & 15) and its keys in the lane's registers, so maxima and sums need two lane swaps
 // and P^T is already laid out as the right operand of O^T = V^T P^T:
 //   bf16: 32 keys a tile, two 16 x 16 score tiles; the P operand wants 8 keys a lane, and
@@ -34,6 +37,11 @@ constexpr int kMaxSplits = 256;  // the join kernel's threads
 //   takes keys 4q + i: again the ones the lane holds, with no packing.
 // Masked scores are -inf; a row that sees no key keeps l = 0 and gives zeros. Values of
 // keys past the end of the sequence are zeroed, whatever the cache holds there.
+// Bound by the read of K and V, each once (counted: 537 and 853 MB). One token over 131000
+// keys, 64 / 8 heads of 128: 82.7 us, 6.5 TB/s (a plain read kernel reaches 5.8 to 6.8); 48
+// requests of up to 8000 keys, 32 / 8 heads: 141.6 us, 6.0 TB/s; non-temporal loads, since
+// nothing is read twice, gave 7% of that. A short call is a chain of dependent reads (lengths
+// and pages, keys, the join), each about a microsecond: 201 keys, 32 heads, 4 us.
 template <int WT, int DH>
 struct AttnTile {
   static constexpr bool kBf = WT == WT_BF16;
@@ -46,8 +54,6 @@ struct AttnTile {
   static constexpr int NO = DH / 16;               // output blocks
 };
 
-typedef __attribute__((ext_vector_type(2))) float f32x2_t;
-
 // Values d4 .. d4 + 3 of one output row, from their unscaled sums and the sum of weights.
 template <int WT, int DH>
 __device__ __forceinline__ void store_row(const AttendArgs& a, int token, int head, int d4, f32x4_t o, float L) {
@@ -58,15 +64,6 @@ __device__ __forceinline__ void store_row(const AttendArgs& a, int token, int he
         (uint64_t)pack_bf16(o[0], o[1]) | (uint64_t)pack_bf16(o[2], o[3]) << 32;
   else
     *reinterpret_cast<SFN_GLOBAL f32x4_t*>(gp(a.out) + at * 4) = o;
-}
-
-__device__ __forceinline__ float wave_max(float v) {
-  v = fmaxf(v, dpp_mov<SFN_DPP_XOR1>(v));
-  v = fmaxf(v, dpp_mov<SFN_DPP_XOR2>(v));
-  v = fmaxf(v, dpp_mov<SFN_DPP_HALF_MIRROR>(v));
-  v = fmaxf(v, dpp_mov<SFN_DPP_ROW_MIRROR>(v));
-  v = swap_pair_max<16>(v);
-  return swap_pair_max<32>(v);
 }
 
 // Whether a word holds a value that is not finite (fp32, or either bf16 half).
@@ -467,6 +464,12 @@ __global__ __launch_bounds__(64 * NW, NW == 8 || RT == 2 ? 2 : 3) void attend_sp
 // The running maximum is raised only when a score passes it by more than kSlack (in log2):
 // softmax does not depend on the number subtracted, 2^8 is far from any overflow in fp32,
 // and most tiles then leave the accumulators alone.
+// Two requests of 2048 tokens after 8192 others, 32 / 8 heads of 128: 619 GFLOP in 580 to 625
+// us by the box, 990 to 1065 TFLOP/s, where a sustained bf16 product of 8192 x 8192 reaches
+// 1385. What bounds it is power: the matrix cores are busy half of the clocks, which fall from
+// 2.2 to 1.8 GHz as the kernel gets better at filling them, and leaving out the whole
+// softmax saves 3%. The four requests' 16-token chunk (82 MB of K and V) reads at 5.8 TB/s
+// between a start of 2 us and the joins.
 typedef __attribute__((ext_vector_type(16))) float f32x16_t;
 typedef __attribute__((ext_vector_type(4))) short i16x4_t;
 #define SFN_LDS __attribute__((address_space(3)))
@@ -482,15 +485,13 @@ __device__ __forceinline__ bf16x8_t read_frag(const SFN_LDS char* p) {
   return *reinterpret_cast<const SFN_LDS bf16x8_t*>(p);
 }
 
-// 16 bytes a lane from base + offset to LDS at lds + 16 lane, without waiting. Written as
-// assembly because the compiler, which cannot tell which LDS the builtin writes, would let
-// every LDS read after it wait for the data. No register is written, so nothing of the
-// compiler's is in flight; whoever reads the LDS waits for vmcnt(0) and a barrier first.
-__device__ __forceinline__ void load_to_lds(const SFN_GLOBAL char* base, uint32_t offset, SFN_LDS char* lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
-               :
-               : "s"((uint32_t)(uintptr_t)lds), "v"(offset), "s"(base)
-               : "memory", "m0");
+// 16 bytes a lane from `from` + offset to LDS at lds + 16 lane, without waiting. A read of LDS
+// afterwards waits for the data unless the compiler can tell that it reads another array: the
+// stages lie in two arrays for that, and the loop takes turns with them (one array: 688 instead
+// of 603 us on the 2048-token prompts, 32.4 instead of 28.9 us on the 16-token chunk). The
+// buffer form, because the waits for LDS are then counted and not for everything (620 and 30.2 us).
+__device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t from, uint32_t offset, SFN_LDS char* lds) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (SFN_LDS void*)lds, 16, offset, 0, 0, 0);
 }
 
 // One wave's state over its 32 rows, and where its lanes read and load.
@@ -514,17 +515,19 @@ struct TileWave {
   // the wave's part of the stage.
   __device__ __forceinline__ static void load(const SFN_GLOBAL char* kp, const SFN_GLOBAL char* vp, SFN_LDS char* kl, SFN_LDS char* vl,
                                               int lane) {
+    const __amdgpu_buffer_rsrc_t kr = __builtin_amdgcn_make_buffer_rsrc((void*)kp, 0, 16 * ROW, 0x00027000);
+    const __amdgpu_buffer_rsrc_t vr = __builtin_amdgcn_make_buffer_rsrc((void*)vp, 0, 16 * ROW, 0x00027000);
 #pragma unroll
     for (int i = 0; i < 16 / RI; ++i) {
       const int row = i * RI + lane / NC, ch = lane % NC;  // the wave's rows start at a multiple of 16
       const uint32_t ko = row * ROW + k_place(row, ch) * 16, vo = row * ROW + v_place(row, ch) * 16;
-      load_to_lds(kp, ko, kl + i * 1024);
-      load_to_lds(vp, vo, vl + i * 1024);
+      load_to_lds(kr, ko, kl + i * 1024);
+      load_to_lds(vr, vo, vl + i * 1024);
     }
   }
 
   // acc += V^T P^T over the stage
-  __device__ __forceinline__ void add_values(const SFN_LDS char* v, const uint32_t (&pw)[2][8]) {
+  __device__ __forceinline__ void add_values(const SFN_LDS char* stage, int voff, const uint32_t (&pw)[2][8]) {
     const int vrow = 4 * h + (c & 15) / 4, vcol = 16 * (c >> 4) + 4 * (c & 3);
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
@@ -534,7 +537,9 @@ struct TileWave {
       for (int d = 0; d < ND; ++d) {
         const int col = 32 * d + vcol;
         // 16 rows further the places repeat
-        const SFN_LDS char* at = v + vrow * ROW + v_place(vrow, col >> 3) * 16 + (col & 7) * 2;
+        int place = voff + vrow * ROW + v_place(vrow, col >> 3) * 16 + (col & 7) * 2;
+        asm("" : "+v"(place));  // one step from the array, so that the compiler sees which array it is
+        const SFN_LDS char* at = stage + place;
         const uint2 x = read_transposed(at + 16 * t * ROW), y = read_transposed(at + (16 * t + 8) * ROW);
         acc[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, make_uint4(x.x, x.y, y.x, y.y)), p, acc[d], 0, 0, 0);
       }
@@ -575,7 +580,7 @@ struct TileWave {
   // The stage's 64 keys from kt on. full: every row sees every key. odd: values that are not
   // finite were taken out of the stage (see add_not_finite).
   template <class Row>
-  __device__ __forceinline__ void step(const SFN_LDS char* k, const SFN_LDS char* v, int kt, bool full, bool odd, float scale_log2,
+  __device__ __forceinline__ void step(const SFN_LDS char* stage, int koff, int voff, int kt, bool full, bool odd, float scale_log2,
                                        Row row, int keys) {
     // the matrix products first: the compute unit's other workgroup then falls out of step and
     // does its softmax meanwhile (614 -> 589 us on the 2048-token prompts)
@@ -587,7 +592,7 @@ struct TileWave {
       for (int i = 0; i < 16; ++i) s[kb][i] = 0.f;
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
-      const SFN_LDS char* at = k + c * ROW + k_place(c, 2 * i + h) * 16;  // the places repeat 32 rows further
+      const SFN_LDS char* at = stage + (koff + c * ROW + k_place(c, 2 * i + h) * 16);  // the places repeat 32 rows further
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb) s[kb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(read_frag(at + 32 * kb * ROW), q[i], s[kb], 0, 0, 0);
     }
@@ -631,7 +636,7 @@ struct TileWave {
       }
     l += add;
     __builtin_amdgcn_s_setprio(1);
-    add_values(v, pw);
+    add_values(stage, voff, pw);
     __builtin_amdgcn_s_setprio(0);
     if (__builtin_expect(odd, 0)) add_not_finite(row, pw, kt, keys);
   }
@@ -645,7 +650,10 @@ __global__ __launch_bounds__(256 * KG, 2) void attend_tile_kernel(AttendArgs a) 
   using W = TileWave<DH>;
   constexpr int ND = W::ND, NC = W::NC, ROW = W::ROW, KT = kTileKeys;
   constexpr int STAGE = KT * ROW;  // bytes of a stage of K, and of V
-  __shared__ __attribute__((aligned(16))) char s_kv[KG * 4 * STAGE];  // a group's K stages, then its V stages
+  // two arrays, so that the compiler knows that the reads of one need not wait for the loads
+  // into the other; of each, a group's K stage and its V stage
+  __shared__ __attribute__((aligned(16))) char s_a[KG * 2 * STAGE];
+  __shared__ __attribute__((aligned(16))) char s_b[KG * 2 * STAGE];
   const int tid = threadIdx.x & 255, lane = threadIdx.x & 63;
   const int kg = KG == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x >> 8);
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);  // in its group
@@ -683,15 +691,12 @@ __global__ __launch_bounds__(256 * KG, 2) void attend_tile_kernel(AttendArgs a) 
   const int k0 = (lo & ~(KT - 1)) + split * a.chunk, k1 = min(k0 + a.chunk, hi);
   if (split > 0 && k0 >= hi) return;
 
-  char* const my = s_kv + kg * 4 * STAGE;
-  SFN_LDS char* const kl = (SFN_LDS char*)my;
-  SFN_LDS char* const vl = kl + 2 * STAGE;
-  const int mine = 16 * wave * ROW;
+  const int group = kg * 2 * STAGE, mine = group + 16 * wave * ROW;
   const int kg0 = k0 + kg * KT;
   if (kg0 < k1) {
     if (lo > 0) page = page_of(kg0);
     const int64_t at = rows_in(page, kg0);
-    W::load(gp(a.k) + at, gp(a.v) + at, kl + mine, vl + mine, lane);
+    W::load(gp(a.k) + at, gp(a.v) + at, (SFN_LDS char*)s_a + mine, (SFN_LDS char*)s_a + STAGE + mine, lane);
   }
 
   // this wave's rows
@@ -721,12 +726,12 @@ __global__ __launch_bounds__(256 * KG, 2) void attend_tile_kernel(AttendArgs a) 
     return gp(a.v) + ((((int64_t)p * a.h_kv + hk) << lg) + (key & pm)) * ROW;
   };
 
-  int buf = 0;
-  for (int kr = k0; kr < k1; kr += KG * KT, buf ^= STAGE) {  // a round: a stage for each group
+  // a round, a stage for each group: the keys from kr on, in cur; the next ones go into nxt
+  auto round = [&](char* cur, char* nxt, int kr) __attribute__((always_inline)) {
     const int kt = kr + kg * KT, kn = kt + KG * KT;
     if (kn < k1) page = page_of(kn);
     // this wave's part of the stage has arrived; after the barrier everyone's has, and the
-    // other buffer is free
+    // other array is free
     __builtin_amdgcn_s_waitcnt(kWaitLoads);
     __syncthreads();
     // A stage with masked keys: what the page holds past the sequence becomes 0, and so do
@@ -734,7 +739,7 @@ __global__ __launch_bounds__(256 * KG, 2) void attend_tile_kernel(AttendArgs a) 
     bool odd = false;
     if (kr + KG * KT > tile_hi || kr < tile_lo) {
       for (int e = kt < k1 ? tid : KT * NC; e < KT * NC; e += 256) {
-        uint4* const at = reinterpret_cast<uint4*>(my + 2 * STAGE + buf + e * 16);
+        uint4* const at = reinterpret_cast<uint4*>(cur + group + STAGE + e * 16);
         const uint4 x = *at;
         if (kt + e / NC >= len) {
           *at = make_uint4(0, 0, 0, 0);
@@ -745,13 +750,19 @@ __global__ __launch_bounds__(256 * KG, 2) void attend_tile_kernel(AttendArgs a) 
       }
       odd = __syncthreads_or(odd);
     }
-    const int nx = buf ^ STAGE;
     if (kn < k1) {
       const int64_t at = rows_in(page, kn);
-      W::load(gp(a.k) + at, gp(a.v) + at, kl + nx + mine, vl + nx + mine, lane);
+      W::load(gp(a.k) + at, gp(a.v) + at, (SFN_LDS char*)nxt + mine, (SFN_LDS char*)nxt + STAGE + mine, lane);
     }
     if (kt < min(some_hi, k1) && kt + KT > some_lo)
-      w.step(kl + buf, vl + buf, kt, kt >= all_lo && kt + KT <= all_hi, odd, a.scale_log2, v_row, min(KT, len - kt));
+      w.step((SFN_LDS char*)cur, group, group + STAGE, kt, kt >= all_lo && kt + KT <= all_hi, odd, a.scale_log2, v_row,
+             min(KT, len - kt));
+  };
+  for (int kr = k0; kr < k1; kr += KG * KT) {
+    round(s_a, s_b, kr);
+    kr += KG * KT;
+    if (kr >= k1) break;
+    round(s_b, s_a, kr);
   }
 
   float l = swap_pair_sum<32>(w.l);
@@ -759,8 +770,8 @@ __global__ __launch_bounds__(256 * KG, 2) void attend_tile_kernel(AttendArgs a) 
   if constexpr (KG == 2) {
     // the second group's sums through LDS, 16 bytes a lane and step, each pair of waves in a
     // part of its own (where the wave below then puts its rows)
-    f32x4_t* const at = reinterpret_cast<f32x4_t*>(s_kv + wave * 32 * DH * 4) + lane;
-    float* const ml = reinterpret_cast<float*>(s_kv + 128 * DH * 4) + 2 * tid;
+    f32x4_t* const at = reinterpret_cast<f32x4_t*>(s_a + wave * 32 * DH * 4) + lane;
+    float* const ml = reinterpret_cast<float*>(s_b) + 2 * tid;
     if (kg == 1) {
 #pragma unroll
       for (int d = 0; d < ND; ++d)
@@ -789,7 +800,7 @@ __global__ __launch_bounds__(256 * KG, 2) void attend_tile_kernel(AttendArgs a) 
   // Rows out through LDS, so that whole rows are written at once (a lane's values are 4 of
   // every 8 of its row). 16-byte places are permuted like the stages'.
   constexpr int OC = DH / 4;  // 16-byte places of an fp32 row
-  char* const out = s_kv + wave * 32 * DH * 4;
+  char* const out = KG == 1 ? (wave < 2 ? s_a : s_b) + (wave & 1) * 32 * DH * 4 : s_a + wave * 32 * DH * 4;
   const bool whole = a.S == 1;
   const float inv = whole ? (l == 0.f ? 0.f : 1.0f / l) : 1.f;
 #pragma unroll
