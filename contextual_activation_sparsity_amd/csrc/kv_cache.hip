@@ -97,8 +97,8 @@ __global__ __launch_bounds__(kPlanThreads) void kv_plan_kernel(KvPlanArgs a) {
   }
   __syncthreads();
   const int T = s_new[R], takes = s_take[R], rels = s_rel[R];
-  const int short_by = takes - rels - n_free;
-  const int status = (s_bad || T > a.max_tokens || n_free + rels > a.n_pages) ? -1 : short_by > 0 ? short_by : 0;
+  // the stack's room is compared first: rels alone may be near 2^31
+  const int status = (s_bad || T > a.max_tokens || rels > a.n_pages - n_free) ? -1 : max(takes - (n_free + rels), 0);
   const bool ok = status == 0;
   // the first workgroups place the tokens, the others everything that goes by request or page:
   // each is a chain of dependent reads, and the chains run side by side

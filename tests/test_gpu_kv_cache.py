@@ -97,6 +97,18 @@ def test_plan_that_cannot_be_done_changes_nothing(held, ctx, new, free, status):
     assert got["pos"] == [0] * 64 and got["slot"] == [-1] * 64
 
 
+def test_plan_counts_of_pages_near_32_bits():
+    R, page, cols, n_pages = 16, 16, 2 ** 27 - 1, 128
+    table = torch.empty((R, cols), dtype=torch.int32, device="cuda")
+    kc = torch.zeros((n_pages, 1, page, 64), dtype=BF, device="cuda")
+    free, n_out, status = i32(list(range(n_pages))), zeros(1), zeros(1)
+    say("[plan] given-back pages and free ones above 2^31 together")
+    B.kv_cache_plan(B.KVCache(kc, kc), i32([cols * page] * R), i32([0] * R), i32([0] * R), table, free, i32([100]), n_out,
+                    zeros(R + 1), zeros(R), zeros(4), zeros(4), status)
+    assert status.item() == -1 and n_out.item() == 100
+    assert free.tolist() == list(range(n_pages))
+
+
 # ---- append --------------------------------------------------------------------------
 
 
