@@ -25,9 +25,10 @@ constexpr int kMaxSplits = 256;  // the join kernel's threads
 // the matrix cores through registers alone: at these sizes the products are far from their
 // bound, and streaming through LDS (as the tile kernel does) took 102 us where this takes
 // 83. Nor do registers for two tiles at once help (105 against 93 us with 8 waves): twelve
-// waves of 16 KB each already keep more than enough bytes under way. The scores are computed as S^T = K Q^T, whose tile leaves one query row per lane
-// (lane & 15) and its keys in the lane's registers, so maxima and sums need two lane swaps
-// and P^T is already laid out as the right operand of O^T = V^T P^T:
+// waves of 16 KB each already keep more than enough bytes under way.
+// The scores are computed as S^T = K Q^T, whose tile leaves one query row per lane (lane & 15)
+// and its keys in the lane's registers, so maxima and sums need two lane swaps and P^T is
+// already laid out as the right operand of O^T = V^T P^T:
 //   bf16: 32 keys a tile, two 16 x 16 score tiles; the P operand wants 8 keys a lane, and
 //   as the order of the contracted keys is free, lane quarter q takes keys 4q..4q+3 of
 //   either score tile, which are the ones it holds. V rows are read as they lie (VW values
@@ -813,7 +814,7 @@ __global__ __launch_bounds__(256 * KG, 2) void attend_tile_kernel(AttendArgs a) 
   const int64_t orow = whole ? (int64_t)(t0 + tok) * a.h_q + head : (((int64_t)r * a.max_new + tok) * a.h_q + head) * a.S + split;
   const int own = ok ? (int)orow : -1;
   if (!whole && h == 0 && ok) *reinterpret_cast<SFN_GLOBAL f32x2_t*>(gp(a.part_ml) + 2 * orow) = f32x2_t{w.m, l};
-  __builtin_amdgcn_wave_barrier();
+  wave_sync();
   constexpr int RO = 64 / OC;  // rows of one step
   const int ch = lane % OC;
 #pragma unroll
@@ -881,7 +882,7 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a) {
     __syncthreads();
     L = (s_red[4] + s_red[5]) + (s_red[6] + s_red[7]);
   } else {
-    __builtin_amdgcn_wave_barrier();
+    wave_sync();
   }
   f32x4_t o = {0.f, 0.f, 0.f, 0.f};
   for (int s = s0; s < used; s += U * NS) {
@@ -895,7 +896,7 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a) {
   }
   f32x4_t* const o_of = s_o + (WAVE ? 64 * wave : 0);
   o_of[tid] = o;
-  if constexpr (WAVE) __builtin_amdgcn_wave_barrier();
+  if constexpr (WAVE) wave_sync();
   else __syncthreads();
   if (tid < LD) {
 #pragma unroll

@@ -24,6 +24,14 @@ __device__ __forceinline__ float wave_max(float v) {
   return swap_pair_max<32>(v);
 }
 
+// Between a wave's writes to LDS and its lanes' reads of each other's: LDS does a wave's
+// accesses in order, so this only keeps the compiler from moving them.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // 2^x by the hardware's exponential (one instruction; results below the smallest normal
 // number flush to zero, which for softmax weights relative to the row's largest is nothing).
 __device__ __forceinline__ float exp2_f(float x) { return __builtin_amdgcn_exp2f(x); }

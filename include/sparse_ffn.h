@@ -368,7 +368,8 @@ int kv_cache_append(const sfn_kv* kv, int32_t T, int32_t h_q, const void* q, int
  *   q        as in kv_cache_append (after it: its q_out);  out [T, h_q, dh]
  *   table    [R, max_pages] (entries are clamped into [0, n_pages)), cu [R + 1], kv_len [R]
  *   max_new, max_len  bounds on every request's new tokens and kv_len (up to 2^30): tokens
- *            past max_new are not computed, keys past max_len or past the table row not read
+ *            past max_new are not computed, keys past max_len or past the table row not read.
+ *            The launch is sized by them: bounds near the real lengths are faster
  *   scale    > 0;  window >= 0 (0: none)
  * Workspace: kv_cache_attend_workspace_size bytes for the same arguments (0 on invalid
  * ones). T = 0 does nothing. Results do not depend on what else runs.
