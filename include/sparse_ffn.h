@@ -364,7 +364,8 @@ int kv_cache_append(const sfn_kv* kv, int32_t T, int32_t h_q, const void* q, int
  *   W > 0 only those with j > P - W,
  * query head h reading key head h / (h_q / h_kv). A token that sees no key (kv_len < n)
  * gives zeros. What a page holds past kv_len is not used, whatever it is. Scores, softmax
- * and sums are fp32; for bf16 the weights are rounded to bf16 before they multiply v.
+ * and sums are fp32; for bf16 the weights are rounded to bf16 before they are summed and
+ * multiply v.
  *   q        as in kv_cache_append (after it: its q_out);  out [T, h_q, dh]
  *   table    [R, max_pages] (entries are clamped into [0, n_pages)), cu [R + 1], kv_len [R]
  *   max_new, max_len  bounds on every request's new tokens and kv_len (up to 2^30): tokens
