@@ -924,12 +924,19 @@ constexpr int kTileFill = 256;
 // 10.1 against 11.2 us for the 888 rows of an fp32 chunk, but 91.5 against 89.8 us for 64 rows
 // of 64 splits.
 constexpr int kJoinByWave = 512;
+// Unsplit items, 8 waves or 4: 256 items of up to 300 keys (32 / 8 heads) 8.5 us with 8; 512
+// items 15.5 with 8, 13.8 with 4 (three workgroups to a compute unit then), 4096 items 92 and 63.
+constexpr int kWideMost = 256;
 
 template <int WT, int DH>
 void launch_sized(const AttendArgs& a, hipStream_t stream) {
   // heads first: the row tiles of a key head lie a multiple of h_kv apart, so that with 8 (or
   // 16, ...) key heads they share an XCD's L2
-  const dim3 grid(a.row_tiles * a.h_kv, a.S, a.R), block(256);
+  // An odd number of splits (the one too many ends at once): workgroups go to the shader
+  // engines in turn, and with 4 splits of ragged lengths one engine would get all the first,
+  // full splits and another all the last ones. 128 requests of up to 8000 keys, 32 / 8 heads,
+  // 4 splits: 477 us without it, 332 with it; 4 splits of 64 requests of up to 3000 100 and 78 us.
+  const dim3 grid(a.row_tiles * a.h_kv, a.S | 1, a.R), block(256);
   if (a.tile_rows == kTileRows) {
     if constexpr (WT == WT_BF16) {
       if ((int64_t)a.R * a.S * a.row_tiles * a.h_kv > kTileFill)
@@ -937,7 +944,8 @@ void launch_sized(const AttendArgs& a, hipStream_t stream) {
       else hipLaunchKernelGGL((attend_tile_kernel<DH, 2>), grid, dim3(512), 0, stream, a);
     }
   } else {
-    const bool wide = a.S == 1;  // one workgroup for all of an item's keys: more waves
+    // one workgroup for all of an item's keys and a compute unit for each: more waves
+    const bool wide = a.S == 1 && (int64_t)a.R * a.row_tiles * a.h_kv <= kWideMost;
     const dim3 threads(wide ? 512 : 256);
     if (a.tile_rows == 16 && wide) hipLaunchKernelGGL((attend_split_kernel<WT, DH, 1, 8>), grid, threads, 0, stream, a);
     else if (a.tile_rows == 16) hipLaunchKernelGGL((attend_split_kernel<WT, DH, 1, 4>), grid, threads, 0, stream, a);
@@ -959,12 +967,14 @@ void launch_sized(const AttendArgs& a, hipStream_t stream) {
 //     heads, takes 86 us with 512, 88 with 768 and 90 with 1024 (with fewer waves to share
 //     the memory with, each streams better, and there are fewer parts to join).
 //   - Several requests: finer, since their lengths differ and the last workgroup is waited
-//     for; splits of kLeast keys, but at most kMost workgroups. 48 requests of up to 8000 keys:
-//     147 us; with splits of 1024 keys 165, with 512 workgroups 190, with 8192 of them 152.
+//     for; down to kLeast keys, but at most kMost workgroups. Each with the other side, 32 / 8
+//     heads, ragged: 8 requests of up to 2000 keys 13.5 us, with splits of 512 16.5; 32 of up to
+//     800 17.3 (20.3); 48 of up to 8000 149, with 2048 workgroups 157, with 4096 149; 256 of up
+//     to 500 (2048 items) 56 unsplit, 63 with 4096 workgroups.
 //   - Up to kWhole keys: no split and no second launch. 32 / 32 heads, each call from Python:
 //     201 keys 5.7 us against 7.7 in two launches, 301 keys 7.2 against 7.7, but 501 keys 10.5
 //     against 8.3 (one compute unit's load rate bounds an unsplit item).
-constexpr int kFill = 512, kLeast = 512, kMost = 4096, kWhole = 384;
+constexpr int kFill = 512, kLeast = 128, kMost = 3200, kWhole = 384;
 AttendPlan attend_plan(int R, int h_q, int h_kv, int dtype, int max_new, int max_len, int window) {
   AttendPlan p{};
   const int64_t rows = (int64_t)max_new * (h_q / h_kv);
