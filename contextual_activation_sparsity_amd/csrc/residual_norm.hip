@@ -4,9 +4,9 @@
 // every input is read once and every output written once, with the two sums of squares
 // (fp32) between. x_out is computed from the fp32 row, before h_out is rounded: each
 // output is rounded once. HBM bound for many tokens: 8192 of 8192 values with both norms and a
-// gate 124 us, 5.4 TB/s where a large copy reaches 5.1 (non-temporal accesses 122 to 127, 256
-// threads of 32 values or 1024 of 8 instead of 512 of 16 130 us). One token of 4096: 2.4 us,
-// the launch, one round of loads and a workgroup-wide sum.
+// gate 124 us, 5.4 TB/s where a large copy reaches 5.1 (non-temporal accesses 122 to 127, gate
+// and weights read before the first sum 128). One token of 4096: 2.8 us back to back in a
+// graph, the launch, one round of loads and the workgroup-wide sums.
 
 #include "kernels.h"
 #include "serving_common.h"
@@ -138,13 +138,28 @@ __global__ __launch_bounds__(NT) void residual_norm_kernel(NormArgs a) {
   }
 }
 
+// One 8-value chunk to a thread where the row allows it: 4000 tokens of 4096 values 32.6 us
+// with 512 threads, 35.5 with 256 of two chunks, one token 2.8 and 3.5 us; 20000 tokens of 512
+// values 21 us with one wave, 34 with 256 threads. Rows past 512 chunks: 8192 values of up to
+// kFewRows tokens with 1024 threads (one token 3.4 us, with 512 threads 3.7), of more with 512
+// (1000 tokens 14.1 us, with 1024 threads 16.5).
+constexpr int kFewRows = 256;
+
+template <int HT, int YT, int WT, int NT, int NV>
+void launch_as(const NormArgs& a, hipStream_t stream) {
+  hipLaunchKernelGGL((residual_norm_kernel<HT, YT, WT, NT, NV>), dim3(a.T), dim3(NT), 0, stream, a);
+}
+
 template <int HT, int YT, int WT>
 void launch_sized(const NormArgs& a, hipStream_t stream) {
   const int nch = a.d / kNormVals;
-  if (nch <= 256) hipLaunchKernelGGL((residual_norm_kernel<HT, YT, WT, 256, 1>), dim3(a.T), dim3(256), 0, stream, a);
-  else if (nch <= 512) hipLaunchKernelGGL((residual_norm_kernel<HT, YT, WT, 256, 2>), dim3(a.T), dim3(256), 0, stream, a);
-  else if (nch <= 1024) hipLaunchKernelGGL((residual_norm_kernel<HT, YT, WT, 512, 2>), dim3(a.T), dim3(512), 0, stream, a);
-  else hipLaunchKernelGGL((residual_norm_kernel<HT, YT, WT, 1024, 2>), dim3(a.T), dim3(1024), 0, stream, a);
+  if (nch <= 64) launch_as<HT, YT, WT, 64, 1>(a, stream);
+  else if (nch <= 128) launch_as<HT, YT, WT, 128, 1>(a, stream);
+  else if (nch <= 256) launch_as<HT, YT, WT, 256, 1>(a, stream);
+  else if (nch <= 512) launch_as<HT, YT, WT, 512, 1>(a, stream);
+  else if (nch <= 1024 && a.T > kFewRows) launch_as<HT, YT, WT, 512, 2>(a, stream);
+  else if (nch <= 1024) launch_as<HT, YT, WT, 1024, 1>(a, stream);
+  else launch_as<HT, YT, WT, 1024, 2>(a, stream);
 }
 
 }  // namespace

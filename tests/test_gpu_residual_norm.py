@@ -56,6 +56,20 @@ def test_residual_norm(h_dt, y_dt, w_dt, post, gated):
         within(xo, X, bx, "x")
 
 
+@pytest.mark.parametrize("T,d,dt", [(257, 4104, BF), (260, 8192, F32), (256, 8184, BF), (300, 512, BF), (70, 1016, F32), (9, 24, BF)])
+def test_residual_norm_many_rows(T, d, dt):
+    say(f"[norm] T={T} d={d} {dt}")
+    g = torch.Generator().manual_seed(d * 7 + T)
+    rnd = lambda s, std=1.0: (torch.randn(s, generator=g) * std).to(dt)  # noqa: E731
+    h, y, w_pre, w_post, gate = rnd((T, d), 2.0), rnd((T, d)), 1 + rnd((d,), 0.2), 1 + rnd((d,), 0.2), rnd((T, d))
+    ho, xo = (torch.full((T, d), float("nan"), dtype=dt, device="cuda") for _ in range(2))
+    B.residual_norm(B.ResidualNorm(w_pre.cuda(), w_post=w_post.cuda(), eps=1e-5, scale=0.5), h.cuda(), y.cuda(), ho, xo, gate=gate.cuda())
+    torch.cuda.synchronize()
+    H, X, bh, bx = bounds(f64(h), f64(y), f64(w_pre), f64(w_post), f64(gate), 0.5, d, dt, dt)
+    within(ho, H, bh, "h")
+    within(xo, X, bx, "x")
+
+
 def test_parts_of_it_and_in_place():
     T, d = 9, 1000
     g = torch.Generator().manual_seed(3)
