@@ -974,6 +974,12 @@ void launch_sized(const AttendArgs& a, hipStream_t stream) {
 //   - Up to kWhole keys: no split and no second launch. 32 / 32 heads, each call from Python:
 //     201 keys 5.7 us against 7.7 in two launches, 301 keys 7.2 against 7.7, but 501 keys 10.5
 //     against 8.3 (one compute unit's load rate bounds an unsplit item).
+//   - Tile kernel: a round of its two wave groups (128 keys) takes as long as writing and joining
+//     kPartsOfRound parts, the second launch as long as kPartsOfJoin; few row tiles are split
+//     if that gains. Split and unsplit: 12 tokens of 3 requests, 8 / 1 heads, 160 keys 12.1 and
+//     11.0 us, 412 keys 12.2 and 14.6; 16 of 8 requests, 32 / 8 heads, 416 keys 16.7 and 15.4,
+//     1016 keys 20.5 and 23.2; a prompt of 400 tokens, 32 / 8 heads, 22.2 and 14.8.
+constexpr int kPartsOfRound = 6500, kPartsOfJoin = 10000;
 constexpr int kFill = 512, kLeast = 128, kMost = 3200, kWhole = 384;
 AttendPlan attend_plan(int R, int h_q, int h_kv, int dtype, int max_new, int max_len, int window) {
   AttendPlan p{};
@@ -994,7 +1000,13 @@ AttendPlan attend_plan(int R, int h_q, int h_kv, int dtype, int max_new, int max
   int64_t span = std::max(1, max_len);
   const int64_t most = std::min<int64_t>(splits(span), (span + step - 1) / step);  // with any window
   if (window > 0) span = std::min<int64_t>(span, (int64_t)window + p.tile_rows + p.tile_keys);
-  const int64_t s = splits(span), chunk = ((span + s - 1) / s + step - 1) / step * step;
+  const int64_t s = splits(span);
+  int64_t chunk = ((span + s - 1) / s + step - 1) / step * step;
+  if (tile && chunk < span) {
+    auto rounds = [](int64_t keys) { return (keys + 2 * kTileKeys - 1) / (2 * kTileKeys); };
+    const int64_t parts = (int64_t)R * max_new * h_q * ((span + chunk - 1) / chunk);
+    if ((rounds(span) - rounds(chunk)) * kPartsOfRound <= kPartsOfJoin + parts) chunk = (span + step - 1) / step * step;
+  }
   p.chunk = (int)chunk;
   p.S = (int)((span + chunk - 1) / chunk);
   p.parts = most > 1 ? (int64_t)R * max_new * h_q * most : 0;
