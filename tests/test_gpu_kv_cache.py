@@ -449,6 +449,35 @@ def test_attend_many_rows_with_splits(dtype, n):
     check_attend(dtype, 16, 4, 64, 16, [(1300, n), (1, 1), (777, n), (0, 0), (1024, n)], seed=24, window=900)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("n", [1, 9])
+def test_attend_unsplit_items_past_the_chip(dtype, n):
+    """More unsplit requests than compute units: four waves to each, in one launch."""
+    rng = random.Random(n)
+    reqs = [(m + rng.choice([0, 1, rng.randint(0, 340)]), m) for m in (rng.choice([0, 1, n, n]) for _ in range(70))]
+    check_attend(dtype, 8, 4, 64, 16, reqs, seed=27)
+    check_attend(dtype, 10, 5, 128, 64, reqs, seed=28, window=100)
+
+
+@pytest.mark.parametrize("lens", [[3000], [2900, 700]])
+def test_attend_infinities_in_split_tiles(lens):
+    """40 tokens of 8 / 1 heads over long sequences: tiles of 128 rows with split keys."""
+    n, R = 40, len(lens)
+    k, v, table = random_cache(lens, 1, 128, 32, BF, 29)
+    q = torch.randn((n * R, 8, 128), generator=torch.Generator().manual_seed(30)).to(BF)
+    say(f"[attend] infinities in split tiles {lens}")
+    cu = [n * r for r in range(R + 1)]
+    clean = run_attend(q, k, v, table, cu, lens)
+    for sl, want, bound in attend_oracle(q, k, v, table, cu, lens, 0, 128 ** -0.5):
+        within(clean[sl], want, bound, f"tokens {sl.start}..{sl.stop}")
+    p = lens[0] - 17  # one of the first request's new tokens
+    v[int(table[0, p // 32]), 0, p % 32, 77] = -float("inf")
+    out = run_attend(q, k, v, table, cu, lens)
+    same = torch.ones(out.shape, dtype=torch.bool, device="cuda")
+    same[n - 17:n, :, 77] = False
+    assert torch.equal(out[same], clean[same]) and (out[~same] == -float("inf")).all()
+
+
 def test_attend_bounds_that_are_too_small():
     """Tokens past max_new are not computed (and not written), keys past max_len not read."""
     lens, cu = [90, 200], [0, 40, 60]
