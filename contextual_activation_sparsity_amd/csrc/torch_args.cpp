@@ -6,8 +6,10 @@
 // raises TypeError or ValueError for a tensor that does not fit, as the other bindings do.
 
 #include <Python.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <exception>
 #include <string>
 
 #include "sparse_ffn.h"
@@ -227,11 +229,25 @@ PyObject* norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 using Fast = PyObject* (*)(PyObject*, PyObject* const*, Py_ssize_t);
-PyCFunction fast(Fast f) { return reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)); }
 
-PyMethodDef methods[] = {{"bind", fast(bind), METH_FASTCALL, nullptr},     {"plan", fast(plan), METH_FASTCALL, nullptr},
-                         {"append", fast(append), METH_FASTCALL, nullptr}, {"attend", fast(attend), METH_FASTCALL, nullptr},
-                         {"norm", fast(norm), METH_FASTCALL, nullptr},     {nullptr, nullptr, 0, nullptr}};
+// F with its C++ exceptions raised as Python's: torch throws for a tensor without storage or
+// strides, and no exception may pass through the interpreter's C frames.
+template <Fast F>
+PyObject* raising(PyObject* self, PyObject* const* a, Py_ssize_t n) noexcept {
+  try {
+    return F(self, a, n);
+  } catch (...) {
+    torch::translate_exception_to_python(std::current_exception());
+    return nullptr;
+  }
+}
+
+template <Fast F>
+PyMethodDef method(const char* name) {
+  return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&raising<F>)), METH_FASTCALL, nullptr};
+}
+PyMethodDef methods[] = {method<bind>("bind"),     method<plan>("plan"), method<append>("append"),
+                         method<attend>("attend"), method<norm>("norm"), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_torch_args", nullptr, -1, methods};
 
 }  // namespace
