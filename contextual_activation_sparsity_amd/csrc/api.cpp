@@ -409,8 +409,8 @@ int check_attend(const sfn_kv* kv, int32_t R, int32_t T, int32_t h_q, int32_t ma
   return SFN_OK;
 }
 
-size_t attend_bytes(const sfn_kv* kv, const sfn::AttendPlan& p) {
-  return sfn::kWsHeader + round256((size_t)p.parts * kv->dh * sizeof(float)) + round256((size_t)p.parts * 2 * sizeof(float));
+size_t attend_bytes(const sfn_kv* kv, int64_t parts) {
+  return sfn::kWsHeader + round256((size_t)parts * kv->dh * sizeof(float)) + round256((size_t)parts * 2 * sizeof(float));
 }
 
 }  // namespace
@@ -491,7 +491,7 @@ size_t kv_cache_attend_workspace_size(const sfn_kv* kv, int32_t R, int32_t T, in
                                       int32_t max_len) {
   try {
     if (check_kv(kv, false) != SFN_OK || check_attend(kv, R, T, h_q, max_new, max_len) != SFN_OK) return 0;
-    return attend_bytes(kv, sfn::attend_plan(R, h_q, kv->h_kv, kv->dtype, max_new, max_len, 0));
+    return attend_bytes(kv, sfn::attend_most_parts(R, h_q, kv->h_kv, kv->dtype, max_new, max_len));
   } catch (...) {
     return 0;
   }
@@ -514,8 +514,8 @@ int kv_cache_attend(const sfn_kv* kv, int32_t R, int32_t T, int32_t h_q, const v
     if (!aligned16(out) || !aligned4_or_null(table) || !aligned4_or_null(cu) || !aligned4_or_null(kv_len)) return SFN_EALIGN;
     if (window >= max_len) window = 0;  // every key is within it
     const sfn::AttendPlan p = sfn::attend_plan(R, h_q, kv->h_kv, kv->dtype, max_new, max_len, window);
-    if ((int64_t)R * p.S * p.row_tiles * kv->h_kv > INT32_MAX || p.parts > INT32_MAX) return SFN_ESHAPE;
-    if ((st = check_ws(ws, ws_bytes, attend_bytes(kv, p))) != SFN_OK) return st;
+    if ((int64_t)R * p.S * p.row_tiles * kv->h_kv > INT32_MAX) return SFN_ESHAPE;
+    if ((st = check_ws(ws, ws_bytes, attend_bytes(kv, p.parts))) != SFN_OK) return st;
     sfn::AttendArgs a{};
     a.k = static_cast<const char*>(kv->k);
     a.v = static_cast<const char*>(kv->v);

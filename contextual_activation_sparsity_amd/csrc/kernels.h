@@ -130,6 +130,8 @@ struct AttendPlan {
   int64_t parts;             // rows of partial results
 };
 AttendPlan attend_plan(int R, int h_q, int h_kv, int dtype, int max_new, int max_len, int window);
+// Rows of partial results that no call within these bounds passes.
+int64_t attend_most_parts(int R, int h_q, int h_kv, int dtype, int max_new, int max_len);
 hipError_t launch_kv_attend(const AttendArgs& a, int dh, int dtype, hipStream_t stream);
 
 struct NormArgs {

@@ -998,7 +998,6 @@ AttendPlan attend_plan(int R, int h_q, int h_kv, int dtype, int max_new, int max
   };
   // keys one row tile can span
   int64_t span = std::max(1, max_len);
-  const int64_t most = std::min<int64_t>(splits(span), (span + step - 1) / step);  // with any window
   if (window > 0) span = std::min<int64_t>(span, (int64_t)window + p.tile_rows + p.tile_keys);
   const int64_t s = splits(span);
   int64_t chunk = ((span + s - 1) / s + step - 1) / step * step;
@@ -1009,8 +1008,26 @@ AttendPlan attend_plan(int R, int h_q, int h_kv, int dtype, int max_new, int max
   }
   p.chunk = (int)chunk;
   p.S = (int)((span + chunk - 1) / chunk);
-  p.parts = most > 1 ? (int64_t)R * max_new * h_q * most : 0;
+  p.parts = p.S > 1 ? (int64_t)R * max_new * h_q * p.S : 0;
   return p;
+}
+
+// A split call launches at most this many workgroups (by the rules above: fewer than 2 kFill, or
+// kMost of several requests; kTileFill of the tile kernel), each with a tile's rows of parts; nor
+// can a row have more splits than its keys have steps. More new tokens may mean fewer parts (up
+// to none), so this is taken over all calls within the bounds.
+int64_t attend_most_parts(int R, int h_q, int h_kv, int dtype, int max_new, int max_len) {
+  const bool bf = dtype == SFN_BF16;
+  const int g = h_q / h_kv;
+  auto parts = [&](int64_t tokens, int64_t keys, int64_t step, int64_t rows_launched) {
+    const int64_t s = std::min<int64_t>((keys + step - 1) / step, kMaxSplits);
+    return s > 1 ? std::min((int64_t)R * tokens * h_q * s, rows_launched) : 0;
+  };
+  const int64_t split = max_len <= kWhole ? 0
+                                          : parts(bf ? std::min(max_new, 32 / g) : max_new, max_len, 4 * (bf ? 32 : 16),
+                                                  32 * (R > 1 ? std::max(2 * kFill, kMost) : 2 * kFill));
+  const int64_t tile = bf && (int64_t)max_new * g > 32 ? parts(max_new, max_len, kTileKeys, (int64_t)kTileRows * kTileFill) : 0;
+  return std::max(split, tile);
 }
 
 hipError_t launch_kv_attend(const AttendArgs& a, int dh, int dtype, hipStream_t stream) {

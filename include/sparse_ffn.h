@@ -372,8 +372,10 @@ int kv_cache_append(const sfn_kv* kv, int32_t T, int32_t h_q, const void* q, int
  *            past max_new are not computed, keys past max_len or past the table row not read.
  *            The launch is sized by them: bounds near the real lengths are faster
  *   scale    > 0;  window >= 0 (0: none)
- * Workspace: kv_cache_attend_workspace_size bytes for the same arguments (0 on invalid
- * ones). T = 0 does nothing. Results do not depend on what else runs.
+ * Workspace: kv_cache_attend_workspace_size bytes for these arguments or larger ones (0 on
+ * invalid ones): what it returns for the largest R, T, max_new and max_len of a program is
+ * enough for every call with smaller ones. T = 0 does nothing. Results do not depend on what
+ * else runs.
  */
 size_t kv_cache_attend_workspace_size(const sfn_kv* kv, int32_t R, int32_t T, int32_t h_q, int32_t max_new,
                                       int32_t max_len);
