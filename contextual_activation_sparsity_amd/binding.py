@@ -5,11 +5,14 @@ torch tensors they are given live on the GPU with the expected dtype and layout,
 their device pointers and the current stream to the library, and raise on a negative
 status. Every step of the computation runs in the library's HIP kernels; PyTorch only
 owns the device memory and the stream. Importing this module fails loudly when the
-library has not been built (``python -m contextual_activation_sparsity_amd.build``).
+library has not been built (``python -m contextual_activation_sparsity_amd.build``); so do
+the paged cache's calls and the norm where their compiled tensor checks have not been.
 """
 
 import ctypes
 import os
+import re
+import sys
 from dataclasses import dataclass
 from typing import Optional
 
@@ -125,13 +128,35 @@ _lib.residual_norm.argtypes = [ctypes.POINTER(sfn_norm), _i32, _vp, _i32, _vp, _
 _lib.residual_norm.restype = ctypes.c_int
 
 
-# the tensor checks of the paged cache's calls and the norm, compiled (csrc/torch_args.cpp)
-try:
-    from . import _torch_args as _args
-except ImportError as e:
-    raise ImportError(f"{e}: build it with `python -m contextual_activation_sparsity_amd.build`") from e
-_args.bind(*(ctypes.cast(f, ctypes.c_void_p).value
+class _NoChecks:
+    """Stands for the compiled tensor checks where they cannot be had."""
+
+    def __init__(self, why):
+        self._why = f"{why}: build it with `python -m contextual_activation_sparsity_amd.build`"
+
+    def __getattr__(self, name):
+        raise ImportError(self._why)
+
+
+def _load_checks():
+    """The tensor checks of the paged cache's calls and the norm, compiled (csrc/torch_args.cpp)
+    for one torch and one Python. The FFN's calls do without them, so a module that is missing
+    or was built for others is reported by the calls that need it."""
+    try:
+        from . import _torch_args as m
+
+        built = (m.TORCH_VERSION, m.PY_VERSION)
+    except (ImportError, AttributeError) as e:
+        return _NoChecks(e)
+    here = (re.match(r"\d+\.\d+\.\d+|", torch.__version__).group(), "%d.%d" % sys.version_info[:2])
+    if built != here:
+        return _NoChecks(f"_torch_args.so is for torch {built[0]} and Python {built[1]}, this is torch {here[0]} and Python {here[1]}")
+    m.bind(*(ctypes.cast(f, ctypes.c_void_p).value
              for f in (_lib.kv_cache_plan, _lib.kv_cache_append, _lib.kv_cache_attend, _lib.residual_norm)))
+    return m
+
+
+_args = _load_checks()
 
 
 class SparseFFNError(RuntimeError):

@@ -8,6 +8,7 @@
 #include <Python.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/version.h>
 
 #include <exception>
 #include <string>
@@ -252,4 +253,14 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_torch_args", nullptr, -1, methods
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__torch_args() { return PyModule_Create(&module); }
+#define SFN_TEXT_OF(x) #x
+#define SFN_TEXT(x) SFN_TEXT_OF(x)
+
+// The module holds for the torch and the Python that it was built against, which the binding compares.
+PyMODINIT_FUNC PyInit__torch_args() {
+  PyObject* m = PyModule_Create(&module);
+  if (m && (PyModule_AddStringConstant(m, "TORCH_VERSION", TORCH_VERSION) < 0 ||
+            PyModule_AddStringConstant(m, "PY_VERSION", SFN_TEXT(PY_MAJOR_VERSION) "." SFN_TEXT(PY_MINOR_VERSION)) < 0))
+    Py_CLEAR(m);
+  return m;
+}
