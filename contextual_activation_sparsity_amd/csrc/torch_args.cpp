@@ -84,6 +84,18 @@ void* pointer(PyObject* o) { return PyLong_AsVoidPtr(o); }
 bool fits(int64_t v, const char* name) { return v <= INT32_MAX || fail(PyExc_ValueError, std::string(name) + " is too large"); }
 PyObject* status(int st) { return PyErr_Occurred() ? nullptr : PyLong_FromLong(st); }
 
+// The status of a library call, during which other Python threads may run (a launch can wait
+// for room in the queue). The caller's arguments keep the tensors and the structure alive. No
+// exception comes out of the library's functions.
+template <class Call>
+PyObject* status_of(Call call) {
+  int st;
+  Py_BEGIN_ALLOW_THREADS
+  st = call();
+  Py_END_ALLOW_THREADS
+  return status(st);
+}
+
 at::ScalarType cache_type(const sfn_kv* kv) { return kv->dtype == SFN_BF16 ? at::kBFloat16 : at::kFloat; }
 at::ScalarType weight_type(const sfn_norm* n) { return n->wdtype == SFN_BF16 ? at::kBFloat16 : at::kFloat; }
 
@@ -124,8 +136,10 @@ PyObject* plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
   void* stream = pointer(a[13]);
   if (PyErr_Occurred()) return nullptr;
   auto i = [&](int k) { return static_cast<int32_t*>(p[k]); };
-  return status(f_plan(kv, (int32_t)R, (int32_t)cols, (int32_t)T, i(1), i(2), i(3), i(4), i(5), i(6), i(7), i(8), i(9), i(10), i(11),
-                       i(12), stream));
+  return status_of([&] {
+    return f_plan(kv, (int32_t)R, (int32_t)cols, (int32_t)T, i(1), i(2), i(3), i(4), i(5), i(6), i(7), i(8), i(9), i(10), i(11), i(12),
+                  stream);
+  });
 }
 
 // (sfn_kv address, k, v, slot, q, q_out, pos, rope, stream)
@@ -154,8 +168,10 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!fits(T, "T") || !fits(h_q, "h_q") || !fits(n_pos, "n_pos") || !fits(rot, "rot")) return nullptr;
   void* stream = pointer(a[8]);
   if (PyErr_Occurred()) return nullptr;
-  return status(f_append(kv, (int32_t)T, (int32_t)h_q, q, qs, k, ks, v, vs, static_cast<int32_t*>(pos), static_cast<int32_t*>(slot),
-                         static_cast<float*>(rope), (int32_t)n_pos, (int32_t)rot, q_out, stream));
+  return status_of([&] {
+    return f_append(kv, (int32_t)T, (int32_t)h_q, q, qs, k, ks, v, vs, static_cast<int32_t*>(pos), static_cast<int32_t*>(slot),
+                    static_cast<float*>(rope), (int32_t)n_pos, (int32_t)rot, q_out, stream);
+  });
 }
 
 // (sfn_kv address, q, table, cu, kv_len, out, ws, max_new, max_len, scale, window, stream)
@@ -188,9 +204,11 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
       !fits(max_len, "max_len") || !fits(window, "window"))
     return nullptr;
   auto clamp = [](long long v) { return (int32_t)(v < -1 ? -1 : v); };
-  return status(f_attend(kv, (int32_t)R, (int32_t)T, (int32_t)h_q, q, qs, static_cast<int32_t*>(table), (int32_t)cols,
-                         static_cast<int32_t*>(cu), static_cast<int32_t*>(kv_len), clamp(max_new), clamp(max_len), (float)scale,
-                         clamp(window), out, ws, ws_bytes, stream));
+  return status_of([&] {
+    return f_attend(kv, (int32_t)R, (int32_t)T, (int32_t)h_q, q, qs, static_cast<int32_t*>(table), (int32_t)cols,
+                    static_cast<int32_t*>(cu), static_cast<int32_t*>(kv_len), clamp(max_new), clamp(max_len), (float)scale,
+                    clamp(window), out, ws, ws_bytes, stream);
+  });
 }
 
 // (sfn_norm address, h, y, h_out, x_out, gate, stream)
@@ -226,7 +244,8 @@ PyObject* norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!fits(T, "T")) return nullptr;
   void* stream = pointer(a[6]);
   if (PyErr_Occurred()) return nullptr;
-  return status(f_norm(nm, (int32_t)T, h, th ? code(*th) : SFN_F32, y, ty ? code(*ty) : SFN_F32, gate, stride, h_out, x_out, stream));
+  const int hdt = th ? code(*th) : SFN_F32, ydt = ty ? code(*ty) : SFN_F32;
+  return status_of([&] { return f_norm(nm, (int32_t)T, h, hdt, y, ydt, gate, stride, h_out, x_out, stream); });
 }
 
 using Fast = PyObject* (*)(PyObject*, PyObject* const*, Py_ssize_t);
