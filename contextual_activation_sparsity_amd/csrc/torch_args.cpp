@@ -227,16 +227,18 @@ PyObject* norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     fail(PyExc_ValueError, "h and y must be bfloat16 or float32");
     return nullptr;
   }
-  const int64_t d = nm->d, T = th ? th->numel() / d : 0;
-  if (th && th->numel() != T * d) {
-    fail(PyExc_ValueError, "h must be [T, " + std::to_string(d) + "]");
-    return nullptr;
-  }
+  // rows of another length are refused, also where their values happen to fill whole rows
+  const int64_t d = nm->d;
+  auto rows = [&](const at::Tensor& t, const char* name) {
+    return (t.dim() > 0 && t.size(-1) == d) || fail(PyExc_ValueError, std::string(name) + " must be [T, " + std::to_string(d) + "]");
+  };
+  if ((th && !rows(*th, "h")) || (ty && !rows(*ty, "y"))) return nullptr;
+  const int64_t T = th ? th->numel() / d : 0;
   int64_t stride = 0;
   if (a[5] != Py_None) {
     const at::Tensor* tg = tensor(a[5], "gate");
-    if (!tg) return nullptr;
-    stride = tg->dim() == 1 && tg->numel() == d ? 0 : d;
+    if (!tg || !rows(*tg, "gate")) return nullptr;
+    stride = tg->dim() == 1 ? 0 : d;
   }
   if (!address(a[2], "y", kAny, T * d, &y) || !address(a[3], "h_out", th ? th->scalar_type() : kAny, T * d, &h_out) ||
       !address(a[4], "x_out", weight_type(nm), T * d, &x_out) || !address(a[5], "gate", weight_type(nm), stride ? T * d : d, &gate))

@@ -37,3 +37,23 @@ def test_one_workspace_for_long_sequences_serves_every_step():
         top = np.abs(want[r]).max()
         assert np.abs(chunk[10 * r:10 * r + 10] - want[r][20:30]).max() < 1e-3 * top
         assert np.abs(one[r] - want[r][30]).max() < 1e-3 * top
+
+
+def test_norm_rows_of_another_length_are_refused():
+    """[4, 32] is not two rows of 64, nor [2, 128] four of them."""
+    bf = dict(dtype=BF, device="cuda")
+    norm = B.ResidualNorm(torch.ones(64, **bf))
+    h, y, x = torch.ones((4, 64), **bf), torch.ones((4, 64), **bf), torch.zeros((4, 64), **bf)
+    wrong = [torch.ones((8, 32), **bf), torch.ones((2, 128), **bf), torch.ones(256, **bf), torch.ones((64, 4), **bf)]
+    for w in wrong:
+        for name, args, kw in (("h", (w, None, None, x), {}), ("y", (h, w, None, x), {}), ("gate", (h, y, None, x), dict(gate=w))):
+            with pytest.raises(ValueError, match=rf"{name} must be \[T, 64\]"):
+                B.residual_norm(norm, *args, **kw)
+    # rows over more dimensions, one row alone, and a longer buffer's first rows stay as they were
+    B.residual_norm(norm, h, y, None, x)
+    again = torch.zeros_like(x)
+    B.residual_norm(norm, h.view(2, 2, 64), torch.cat([y, y]), None, again, gate=torch.ones(64, **bf))
+    one = torch.zeros(64, **bf)
+    B.residual_norm(norm, h[0], y[0], None, one)
+    torch.cuda.synchronize()
+    assert torch.equal(x, again) and torch.equal(one, x[0])
