@@ -807,6 +807,7 @@ __global__ __launch_bounds__(256 * KG, 2) void attend_tile_kernel(AttendArgs a) 
 #pragma unroll
         for (int j = 0; j < 4; ++j) w.acc[d][4 * e + j] = w.acc[d][4 * e + j] * f + o[j] * fo;
       }
+    wave_sync();  // the rows below go where other lanes read these sums
   }
   // Rows out through LDS, so that whole rows are written at once (a lane's values are 4 of
   // every 8 of its row). 16-byte places are permuted like the stages'.

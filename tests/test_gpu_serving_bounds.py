@@ -57,3 +57,14 @@ def test_norm_rows_of_another_length_are_refused():
     B.residual_norm(norm, h[0], y[0], None, one)
     torch.cuda.synchronize()
     assert torch.equal(x, again) and torch.equal(one, x[0])
+
+
+@pytest.mark.parametrize("dh", [64, 128])
+@pytest.mark.parametrize("scale", [None, 2.0])
+def test_attend_two_groups_join(dh, scale):
+    """Tiles of 128 rows whose keys two groups of waves share, split and whole, with stages for
+    both, for one alone, and maxima far apart (one group's sums all but vanish): each wave's
+    rows go through the LDS that it has just read the other group's sums from."""
+    for reqs in ([(700, 16), (129, 16), (64, 16), (65, 16)], [(16, 16)], [(130, 100), (1000, 100)], [(5000, 24), (40, 40)]):
+        check_attend(BF, 16, 2, dh, 64, reqs, seed=31, scale=scale)
+        check_attend(BF, 9, 1, dh, 16, reqs, seed=32, scale=scale, window=150)
