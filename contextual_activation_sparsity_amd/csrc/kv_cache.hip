@@ -53,7 +53,9 @@ __global__ __launch_bounds__(kPlanThreads) void kv_plan_kernel(KvPlanArgs a) {
   int* const s_rel = s_cu + 2 * (R + 1);
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   if (tid == 0) s_bad = 0;
-  const int n_free = min(max(gp(a.n_free)[0], 0), a.n_pages);
+  const int given = gp(a.n_free)[0];
+  const bool counted = given >= 0 && given <= a.n_pages;
+  const int n_free = counted ? given : 0;
   __syncthreads();
   const int per = (R + kPlanThreads - 1) / kPlanThreads;
   const int r0 = tid * per, r1 = min(R, r0 + per);
@@ -100,7 +102,7 @@ __global__ __launch_bounds__(kPlanThreads) void kv_plan_kernel(KvPlanArgs a) {
   __syncthreads();
   const int T = s_new[R], takes = s_take[R], rels = s_rel[R];
   // the stack's room is compared first: rels alone may be near 2^31
-  const int status = (s_bad || T > a.max_tokens || rels > a.n_pages - n_free) ? -1 : max(takes - (n_free + rels), 0);
+  const int status = (s_bad || !counted || T > a.max_tokens || rels > a.n_pages - n_free) ? -1 : max(takes - (n_free + rels), 0);
   const bool ok = status == 0;
   // the first workgroups place the tokens, the others everything that goes by request or page:
   // each is a chain of dependent reads, and the chains run side by side
@@ -146,7 +148,7 @@ __global__ __launch_bounds__(kPlanThreads) void kv_plan_kernel(KvPlanArgs a) {
   }
   if (gid == 0) {
     gp(a.cu)[0] = 0;
-    gp(a.n_free_out)[0] = ok ? n_free + rels - takes : n_free;
+    gp(a.n_free_out)[0] = ok ? n_free + rels - takes : given;
     gp(a.status)[0] = status;
   }
 }

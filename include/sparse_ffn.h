@@ -326,9 +326,10 @@ typedef struct sfn_kv {
  *   pos, slot  [max_tokens], written: past the last token 0 and -1
  *   status     1 int32, written: 0; the number of pages missing; or -1 for lengths that
  *              are negative, longer than a table row or than held_len, more than max_tokens
- *              tokens, or a stack that would outgrow n_pages. Unless 0 nothing is taken or
- *              given back (table and stack unchanged, *n_free_out = *n_free), cu and kv_len
- *              are 0 and every slot -1, so the calls after it write and attend to nothing.
+ *              tokens, *n_free below 0 or above n_pages, or a stack that would outgrow
+ *              n_pages. Unless 0 nothing is taken or given back (table and stack unchanged,
+ *              *n_free_out = *n_free), cu and kv_len are 0 and every slot -1, so the calls
+ *              after it write and attend to nothing.
  * Outputs must not overlap inputs. Planning the same inputs again gives the same result.
  * R <= 4096, max_tokens <= 262144.
  */

@@ -17,7 +17,7 @@ def cache_plan(page, table, free_pages, n_free, held, ctx, new, n_pages, max_tok
     for h, c, n in zip(held, ctx, new):
         if h < 0 or c < 0 or n < 0 or c > h or h > cap * page or c + n > cap * page:
             return {"status": -1}
-    if sum(new) > max_tokens:
+    if sum(new) > max_tokens or not 0 <= n_free <= n_pages:
         return {"status": -1}
     stack = list(free_pages[:n_free])
     rows = [list(r) for r in table]

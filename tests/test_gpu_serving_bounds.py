@@ -68,3 +68,16 @@ def test_attend_two_groups_join(dh, scale):
     for reqs in ([(700, 16), (129, 16), (64, 16), (65, 16)], [(16, 16)], [(130, 100), (1000, 100)], [(5000, 24), (40, 40)]):
         check_attend(BF, 16, 2, dh, 64, reqs, seed=31, scale=scale)
         check_attend(BF, 9, 1, dh, 16, reqs, seed=32, scale=scale, window=150)
+
+
+@pytest.mark.parametrize("n_free", [-1, -2 ** 31, 9, 2 ** 31 - 1])
+@pytest.mark.parametrize("held,ctx,new", [([16], [16], [1]), ([16], [3], [1]), ([32], [0], [0])])
+def test_plan_with_a_count_of_free_pages_that_cannot_be(n_free, held, ctx, new):
+    """Of 8 pages: refused as a whole, the count handed on as it came."""
+    say(f"[plan] n_free {n_free} {held} {ctx} {new}")
+    table, stack = [[1, 2, -9, -9]], [3, 4, 5, 6, 7, 0]
+    assert S.cache_plan(16, table, stack, n_free, held, ctx, new, 8, 4) == {"status": -1}
+    got = run_plan(16, table, stack, n_free, held, ctx, new, 8, 4)
+    assert got["status"] == [-1] and got["n_out"] == [n_free]
+    assert got["table"] == table and got["free"] == stack + [-1, -1]
+    assert got["cu"] == [0, 0] and got["kv_len"] == [0] and got["pos"] == [0] * 4 and got["slot"] == [-1] * 4
