@@ -369,9 +369,13 @@ int kv_cache_append(const sfn_kv* kv, int32_t T, int32_t h_q, const void* q, int
  * multiply v.
  *   q        as in kv_cache_append (after it: its q_out);  out [T, h_q, dh]
  *   table    [R, max_pages] (entries are clamped into [0, n_pages)), cu [R + 1], kv_len [R]
- *   max_new, max_len  bounds on every request's new tokens and kv_len (up to 2^30): tokens
- *            past max_new are not computed, keys past max_len or past the table row not read.
- *            The launch is sized by them: bounds near the real lengths are faster
+ *   max_new, max_len  bounds on every request's new tokens and kv_len (up to 2^30). Lengths
+ *            past them are not an error that can be reported, and stay in bounds: tokens past
+ *            max_new are not computed (the others are, as if the bound were right), and a
+ *            request whose kv_len is past max_len, or past its table row, is taken to end
+ *            there: kv_len counts as that bound, also in P, so all its results are those of
+ *            the shorter request. The launch is sized by the bounds: near the real lengths
+ *            they are faster
  *   scale    > 0;  window >= 0 (0: none)
  * Workspace: kv_cache_attend_workspace_size bytes for these arguments or larger ones (0 on
  * invalid ones): what it returns for the largest R, T, max_new and max_len of a program is

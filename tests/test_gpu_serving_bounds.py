@@ -81,3 +81,37 @@ def test_plan_with_a_count_of_free_pages_that_cannot_be(n_free, held, ctx, new):
     assert got["status"] == [-1] and got["n_out"] == [n_free]
     assert got["table"] == table and got["free"] == stack + [-1, -1]
     assert got["cu"] == [0, 0] and got["kv_len"] == [0] and got["pos"] == [0] * 4 and got["slot"] == [-1] * 4
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("window", [0, 60])
+@pytest.mark.parametrize("lens,cu,h_q,max_len,cols", [
+    ([200, 90], [0, 20, 23], 4, 100, None), ([200, 90], [0, 150, 153], 4, 100, None), ([1900, 700], [0, 30, 31], 8, 1000, None),
+    ([900, 40], [0, 1, 2], 4, 900, 33), ([900, 40], [0, 100, 101], 16, 2 ** 30, 33)])
+def test_attend_of_requests_past_a_bound_is_of_the_shorter_request(dtype, window, lens, cu, h_q, max_len, cols):
+    """kv_len past max_len, or past a table row of `cols` pages, counts as that bound: positions,
+    causal limits and windows are the shorter request's, in every kernel."""
+    k, v, table = random_cache(lens, 2, 64, 16, dtype, 33)
+    if cols:
+        table = table[:, :cols].contiguous()
+    q = torch.randn((cu[-1], h_q, 64), generator=torch.Generator().manual_seed(34)).to(dtype)
+    say(f"[attend] past the bounds, {dtype} window={window} {lens} max_len={max_len} cols={cols}")
+    out = run_attend(q, k, v, table, cu, lens, window, max_len=max_len)
+    cut = [min(n, max_len, 16 * table.shape[1]) for n in lens]
+    assert cut[0] < lens[0]
+    for sl, want, bound in attend_oracle(q, k, v, table, cu, cut, window, 64 ** -0.5):
+        within(out[sl], want, bound, f"tokens {sl.start}..{sl.stop}")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_attend_tokens_past_max_new_leave_the_others(dtype):
+    """max_new too small: the tokens that are computed have their own positions."""
+    lens, cu = [300, 120], [0, 40, 45]
+    k, v, table = random_cache(lens, 2, 64, 16, dtype, 35)
+    q = torch.randn((45, 4, 64), generator=torch.Generator().manual_seed(36)).to(dtype)
+    for max_new, window in ((1, 0), (7, 50), (39, 0)):
+        say(f"[attend] max_new {max_new} window {window} {dtype}")
+        out = run_attend(q, k, v, table, cu, lens, window, max_new=max_new)
+        for sl, want, bound in attend_oracle(q, k, v, table, cu, lens, window, 64 ** -0.5):
+            within(out[sl][:max_new], want[:max_new], bound[:max_new], "computed tokens")
+            assert torch.isnan(out[sl][max_new:]).all()
