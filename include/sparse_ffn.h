@@ -377,6 +377,10 @@ int kv_cache_append(const sfn_kv* kv, int32_t T, int32_t h_q, const void* q, int
  *            the shorter request. The launch is sized by the bounds: near the real lengths
  *            they are faster
  *   scale    > 0;  window >= 0 (0: none)
+ * The work is divided as if every request had max_new tokens. Where requests of one or a few
+ * tokens stand beside longer ones, a call for each kind is faster, with a max_new of its own
+ * and the same q, out and T: for requests [r0, r1) the R = r1 - r0 rows of table from r0 on,
+ * cu + r0 (still offsets into all T tokens) and kv_len + r0.
  * Workspace: kv_cache_attend_workspace_size bytes for these arguments or larger ones (0 on
  * invalid ones): what it returns for the largest R, T, max_new and max_len of a program is
  * enough for every call with smaller ones. T = 0 does nothing. Results do not depend on what

@@ -115,3 +115,24 @@ def test_attend_tokens_past_max_new_leave_the_others(dtype):
         for sl, want, bound in attend_oracle(q, k, v, table, cu, lens, window, 64 ** -0.5):
             within(out[sl][:max_new], want[:max_new], bound[:max_new], "computed tokens")
             assert torch.isnan(out[sl][max_new:]).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_attend_of_some_requests_at_a_time(dtype):
+    """A step of prompts, chunks and single tokens in a call for each kind: parts of the page
+    table, of cu (offsets into all tokens) and of the lengths, one output."""
+    lens, news = [900, 33, 1500, 1, 70, 260, 420], [1, 1, 1, 1, 16, 9, 200]
+    cu = [0]
+    for n in news:
+        cu.append(cu[-1] + n)
+    k, v, table = random_cache(lens, 2, 128, 32, dtype, 37)
+    q = torch.randn((cu[-1], 8, 128), generator=torch.Generator().manual_seed(38)).to(dtype)
+    cache, qd, td, cd, ld = B.KVCache(k.cuda(), v.cuda()), q.cuda(), table.cuda(), i32(cu), i32(lens)
+    out = torch.full(q.shape, float("nan"), dtype=dtype, device="cuda")
+    ws = B.workspace(B.kv_cache_attend_workspace_size(cache, len(lens), cu[-1], 8, 200, 1500))
+    for r0, r1, n in ((0, 4, 1), (4, 6, 16), (6, 7, 200)):
+        say(f"[attend] requests {r0} to {r1} of a mixed step, {dtype}")
+        B.kv_cache_attend(cache, qd, td[r0:r1], cd[r0:r1 + 1], ld[r0:r1], out, ws, n, 1500)
+    torch.cuda.synchronize()
+    for sl, want, bound in attend_oracle(q, k, v, table, cu, lens, 0, 128 ** -0.5):
+        within(out[sl], want, bound, f"tokens {sl.start}..{sl.stop}")
