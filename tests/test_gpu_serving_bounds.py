@@ -136,3 +136,12 @@ def test_attend_of_some_requests_at_a_time(dtype):
     torch.cuda.synchronize()
     for sl, want, bound in attend_oracle(q, k, v, table, cu, lens, 0, 128 ** -0.5):
         within(out[sl], want, bound, f"tokens {sl.start}..{sl.stop}")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("dh,n_keys", [(64, 9500), (64, 20001), (64, 32768), (128, 32768)])
+def test_attend_most_splits(dtype, dh, n_keys):
+    """One token of one head over a long sequence: up to the 256 splits that there are at most,
+    for which the join reads its parts in several rounds."""
+    check_attend(dtype, 1, 1, dh, 64, [(n_keys, 1)], seed=39)
+    check_attend(dtype, 2, 1, dh, 64, [(n_keys, 3)], seed=40)
