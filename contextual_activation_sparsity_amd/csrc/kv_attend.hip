@@ -38,11 +38,15 @@ constexpr int kMaxSplits = 256;  // the join kernel's threads
 //   takes keys 4q + i: again the ones the lane holds, with no packing.
 // Masked scores are -inf; a row that sees no key keeps l = 0 and gives zeros. Values of
 // keys past the end of the sequence are zeroed, whatever the cache holds there.
-// Bound by the read of K and V, each once (counted: 537 and 853 MB). One token over 131000
-// keys, 64 / 8 heads of 128: 82.7 us, 6.5 TB/s (a plain read kernel reaches 5.8 to 6.8); 48
-// requests of up to 8000 keys, 32 / 8 heads: 141.6 us, 6.0 TB/s; non-temporal loads, since
-// nothing is read twice, gave 7% of that. A short call is a chain of dependent reads (lengths
-// and pages, keys, the join), each about a microsecond: 201 keys, 32 heads, 4 us.
+// Rows of one tile: bound by the read of K and V, each once (counted: 537 and 853 MB). One token
+// over 131000 keys, 64 / 8 heads of 128: 82.7 us, 6.5 TB/s (a plain read kernel reaches 5.8 to
+// 6.8); 48 requests of up to 8000 keys, 32 / 8 heads: 141.6 us, 6.0 TB/s; non-temporal loads,
+// since nothing is read twice, gave 7% of that. fp32 twice the bytes: 168 and 272 us. A short call
+// is a chain of dependent reads (lengths and pages, keys, the join), each about a microsecond:
+// 201 keys, 32 heads, 4 us.
+// fp32 with more rows reads K and V again for every tile of 32, and is bound by the products,
+// which wait for each tile's loads: two requests of 1000 tokens after 4000 others, 32 / 8 heads
+// of 128, 1387 us, 106 TFLOP/s where an fp32 product of 8192 x 8192 reaches 154.
 template <int WT, int DH>
 struct AttnTile {
   static constexpr bool kBf = WT == WT_BF16;
@@ -474,13 +478,19 @@ __global__ __launch_bounds__(64 * NW, NW == 8 || RT == 2 ? 2 : 3) void attend_sp
 // addresses that are permuted.
 // The running maximum is raised only when a score passes it by more than kSlack (in log2):
 // softmax does not depend on the number subtracted, 2^8 is far from any overflow in fp32,
-// and most tiles then leave the accumulators alone.
+// and most tiles then leave the accumulators alone. It costs accuracy where one key has most of
+// the weight: with the exact maximum that key's weight is 1, which bf16 holds exactly, with a
+// lagging one it is rounded like the others. Sharp scores (deviation 2), error against 64 bits
+// relative to the result: 0.0021 for the 16-token chunk and 0.0022 for prompts; with kSlack 0
+// 0.0018 and 0.0019, like the split kernel, and 1 to 4% longer for chunks, 6 to 9% for prompts.
 // Two requests of 2048 tokens after 8192 others, 32 / 8 heads of 128: 619 GFLOP in 580 to 625
 // us by the box, 990 to 1065 TFLOP/s, where a sustained bf16 product of 8192 x 8192 reaches
-// 1385. What bounds it is power: the matrix cores are busy half of the clocks, which fall from
-// 2.2 to 1.8 GHz as the kernel gets better at filling them, and leaving out the whole
-// softmax saves 3%. The four requests' 16-token chunk (82 MB of K and V) reads at 5.8 TB/s
-// between a start of 2 us and the joins.
+// 1385. What bounds it is power, and how full the matrix cores are: they are busy half of the
+// clocks (the library's product keeps them busy 69%), with no bank conflict in LDS, and the
+// clock falls to 1.6 to 1.9 GHz, as it does for that product, where a kernel bound by memory runs
+// at 2.5. Fewer clocks a key have brought lower clocks: leaving out the whole softmax saves 3%.
+// Heads of 64 have as much softmax for half the products: 370 us, 837 TFLOP/s. The four requests'
+// 16-token chunk (82 MB of K and V) reads at 5.8 TB/s between a start of 2 us and the joins.
 typedef __attribute__((ext_vector_type(16))) float f32x16_t;
 typedef __attribute__((ext_vector_type(4))) short i16x4_t;
 #define SFN_LDS __attribute__((address_space(3)))
@@ -917,9 +927,11 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a) {
 }
 
 // Tile kernel: up to this many workgroups get two groups of waves (one to a compute unit),
-// and few row tiles are split into about as many. The 16-token chunk of four requests, 64 / 8
-// heads, up to 6000 keys: 28.7 us, with 384 or 512 splits 41 and 40 (before a row's parts were
-// joined by one wave).
+// and few row tiles are split into at most as many. 16-token chunks of R requests, 64 / 8 heads,
+// ragged up to 4000 keys, with 256 workgroups at most, with 384 and with 512 (then one group of
+// waves and two workgroups to a compute unit): R = 4 24.6, 27.4 and 26.4 us; 8 36.8, 41.8, 39.8;
+// 12 54.8, 57.1, 52.0; 16 58.4, 69.1, 62.3; 17 77.9, 87.0, 71.2; 24 81.5, 95.5, 95.3. The division
+// is of whole row tiles, so that 17 requests are 136 workgroups where 16 are 256.
 constexpr int kTileFill = 256;
 // From so many rows on a wave joins one instead of a workgroup: 28.7 against 31.8 us there,
 // 10.1 against 11.2 us for the 888 rows of an fp32 chunk, but 91.5 against 89.8 us for 64 rows
