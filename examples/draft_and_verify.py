@@ -65,6 +65,8 @@ class Decoder:
         """Runs tokens[r] (a list for each request) after the first keep[r] tokens of request r;
         returns the logits of all of them, one request after the other."""
         new = [len(t) for t in tokens]
+        if max(k + n for k, n in zip(keep, new)) > self.max_len:
+            raise ValueError(f"a sequence of more than max_len = {self.max_len} tokens, drafts counted")
         T = sum(new)
         dev = lambda v, dt=torch.int32: torch.tensor(v, dtype=dt, device="cuda")  # noqa: E731
         pos, slot = (torch.empty(T, dtype=torch.int32, device="cuda") for _ in range(2))

@@ -145,3 +145,15 @@ def test_attend_most_splits(dtype, dh, n_keys):
     for which the join reads its parts in several rounds."""
     check_attend(dtype, 1, 1, dh, 64, [(n_keys, 1)], seed=39)
     check_attend(dtype, 2, 1, dh, 64, [(n_keys, 3)], seed=40)
+
+
+def test_example_refuses_sequences_past_its_tables():
+    """A plan that cannot be done leaves the step without tokens, and its logits without meaning:
+    the example stops before it. 36 tokens and 16 drafts past them fill a table of 52."""
+    m = load()
+    model = m.Decoder(max_len=52, requests=2)
+    seqs, _, _ = model.generate([[1, 2, 3], [4] * 30], 6)
+    assert [len(s) for s in seqs] == [9, 36] and model.status.item() == 0
+    model = m.Decoder(max_len=44, requests=2)
+    with pytest.raises(ValueError, match="max_len = 44"):
+        model.generate([[1, 2, 3], [4] * 30], 6)
