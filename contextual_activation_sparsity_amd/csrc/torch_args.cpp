@@ -1,6 +1,6 @@
 // The binding's argument marshalling for the calls that a decode step makes several times in
 // every layer: torch tensors checked (device, dtype, layout, size) and turned into addresses
-// here instead of in Python, where that takes longer than the kernels (plan 8.6 -> 4.5 us a
+// here instead of in Python, where that takes longer than the kernels (plan 8.6 -> 4.2 us a
 // call on an MI355X's host). The C functions are those that the ctypes binding has loaded;
 // their addresses are handed over at import. Every function returns the call's status, or
 // raises TypeError or ValueError for a tensor that does not fit, as the other bindings do.
