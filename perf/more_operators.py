@@ -9,7 +9,7 @@ shared   attention of requests whose first tokens are the same (a system prompt,
          which are read once for all of them; over a cache in the model's type or in 8 bits
 
 A row's power of two is held as one byte b for 2^(b - 127): the smallest one with which the row's
-largest magnitude is at most 448 (the largest e4m3 value), 10 at least and 247 at most.
+largest magnitude is at most 448 (the largest e4m3 value), 10 at least and 246 at most.
 
 Sequence lengths are a function of the case; the seed makes the values and the pages' places.
 """
@@ -289,7 +289,7 @@ def _quantise(x):
     nearest, ties to the even one. In 64 bits, where values stand next to a border."""
     a = x.abs().amax(-1)
     m, e = torch.frexp(a)
-    b = torch.where(a > 0, e + 127 - 9 + (m > 0.875).to(e.dtype), 0).clamp(10, 247)
+    b = torch.where(a > 0, e + 127 - 9 + (m > 0.875).to(e.dtype), 0).clamp(10, 246)
     y = torch.ldexp(x, 127 - b[..., None])
     step = torch.ldexp(torch.ones_like(y), (torch.frexp(y)[1] - 1).clamp(min=-6) - 3)
     return (torch.round(y / step) * step).float().to(E4M3), b.to(torch.uint8)
@@ -452,7 +452,7 @@ def _exact_append8(case, s):
 
     out, slot = {"q_out": turn(s["q"])}, s["slot"].long()
     for n, x in (("k", turn(s["k"])), ("v", s["v"].double())):
-        b = torch.ceil(torch.log2(x.abs().amax(-1, keepdim=True) / 448)).clamp(-117, 120)
+        b = torch.ceil(torch.log2(x.abs().amax(-1, keepdim=True) / 448)).clamp(-117, 119)
         flat = _stand_for(s[n + "_cache"]).permute(0, 2, 1, 3).reshape(-1, case["h_kv"], case["dh"])
         flat = flat.index_copy(0, slot, x / 2.0 ** b)
         out[n + "_cache"] = flat.reshape(-1, p, case["h_kv"], case["dh"]).permute(0, 2, 1, 3).contiguous()
