@@ -57,6 +57,14 @@ EXPORTED = (
     "kv_cache_attend_workspace_size",
     "kv_cache_attend",
     "residual_norm",
+    "kv_cache_attend_shared_workspace_size",
+    "kv_cache_attend_shared",
+    "kv8_cache_append",
+    "kv8_cache_read",
+    "kv8_cache_attend_workspace_size",
+    "kv8_cache_attend",
+    "kv8_cache_attend_shared_workspace_size",
+    "kv8_cache_attend_shared",
 )
 
 
@@ -80,6 +88,10 @@ class sfn_kv(ctypes.Structure):
         ("n_pages", ctypes.c_int32), ("page", ctypes.c_int32), ("h_kv", ctypes.c_int32), ("dh", ctypes.c_int32),
         ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
     ]
+
+
+class sfn_kv8(ctypes.Structure):
+    _fields_ = [("kv", sfn_kv), ("k_exp", ctypes.c_void_p), ("v_exp", ctypes.c_void_p)]
 
 
 class sfn_norm(ctypes.Structure):
@@ -124,6 +136,16 @@ _lib.kv_cache_attend_workspace_size.restype = _sz
 _lib.kv_cache_attend.argtypes = [ctypes.POINTER(sfn_kv), _i32, _i32, _i32, _vp, _i64, _vp, _i32, _vp, _vp, _i32, _i32, _f32,
                                  _i32, _vp, _vp, _sz, _vp]
 _lib.kv_cache_attend.restype = ctypes.c_int
+_lib.kv_cache_attend_shared_workspace_size.argtypes = [ctypes.POINTER(sfn_kv)] + [_i32] * 6
+_lib.kv_cache_attend_shared_workspace_size.restype = _sz
+_lib.kv_cache_attend_shared.argtypes = [ctypes.POINTER(sfn_kv), _i32, _i32, _i32, _vp, _i64, _vp, _i32, _vp, _vp, _i32, _vp, _vp,
+                                        _i32, _i32, _i32, _f32, _vp, _vp, _sz, _vp]
+_lib.kv_cache_attend_shared.restype = ctypes.c_int
+for _name in ("append", "attend_workspace_size", "attend", "attend_shared_workspace_size", "attend_shared"):
+    _f, _g = getattr(_lib, "kv8_cache_" + _name), getattr(_lib, "kv_cache_" + _name)
+    _f.argtypes, _f.restype = [ctypes.POINTER(sfn_kv8)] + _g.argtypes[1:], _g.restype
+_lib.kv8_cache_read.argtypes = [ctypes.POINTER(sfn_kv8), _i32, _vp, _vp, _i64, _vp, _i64, _vp]
+_lib.kv8_cache_read.restype = ctypes.c_int
 _lib.residual_norm.argtypes = [ctypes.POINTER(sfn_norm), _i32, _vp, _i32, _vp, _i32, _vp, _i64, _vp, _vp, _vp]
 _lib.residual_norm.restype = ctypes.c_int
 
@@ -151,8 +173,12 @@ def _load_checks():
     here = (re.match(r"\d+\.\d+\.\d+|", torch.__version__).group(), "%d.%d" % sys.version_info[:2])
     if built != here:
         return _NoChecks(f"_torch_args.so is for torch {built[0]} and Python {built[1]}, this is torch {here[0]} and Python {here[1]}")
-    m.bind(*(ctypes.cast(f, ctypes.c_void_p).value
-             for f in (_lib.kv_cache_plan, _lib.kv_cache_append, _lib.kv_cache_attend, _lib.residual_norm)))
+    if not hasattr(m, "bind_more"):
+        return _NoChecks("_torch_args.so is older than this binding")
+    for bind, calls in ((m.bind, (_lib.kv_cache_plan, _lib.kv_cache_append, _lib.kv_cache_attend, _lib.residual_norm)),
+                        (m.bind_more, (_lib.kv8_cache_append, _lib.kv8_cache_read, _lib.kv8_cache_attend,
+                                       _lib.kv_cache_attend_shared, _lib.kv8_cache_attend_shared))):
+        bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in calls))
     return m
 
 
@@ -195,6 +221,18 @@ def _stream(stream):
         # torch.cuda.current_stream().cuda_stream without building a Stream object (2.8 us)
         return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _place(kv, stream):
+    """The stream's address and the current device, on which the cache and the call's tensors have to be."""
+    device = torch._C._cuda_getDevice()
+    if kv.device != device:
+        raise ValueError(f"the cache is on cuda:{kv.device}, the current device is cuda:{device}")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device), device
+    if getattr(stream, "device_index", device) != device:
+        raise ValueError(f"the stream is of cuda:{stream.device_index}, the current device is cuda:{device}")
+    return _stream(stream), device
 
 
 _WDT = {torch.bfloat16: SFN_BF16, torch.float32: SFN_F32}
@@ -370,10 +408,39 @@ class KVCache:
         if self.k.dtype not in _WDT:
             raise ValueError("the cache must be bfloat16 or float32")
         self.n_pages, self.h_kv, self.page, self.dh = self.k.shape
-        self.dtype = self.k.dtype
+        self.dtype, self.device = self.k.dtype, self.k.device.index
         self.c = sfn_kv(self.n_pages, self.page, self.h_kv, self.dh, _WDT[self.dtype], 0, _ptr(self.k, "k"),
                         _ptr(self.v, "v"))
         self.addr = ctypes.addressof(self.c)
+
+
+@dataclass
+class KVCache8:
+    """One layer's paged key/value cache in 8 bits: k and v [n_pages, h_kv, page, dh]
+    float8_e4m3fn codes, k_exp and v_exp [n_pages, h_kv, page] uint8 (a row's values are its
+    codes times 2^(byte - 127)), and the dtype of the tokens it serves (bfloat16 or float32).
+    kv_cache_plan takes it as it takes a KVCache."""
+
+    k: torch.Tensor
+    v: torch.Tensor
+    k_exp: torch.Tensor
+    v_exp: torch.Tensor
+    dtype: torch.dtype = torch.bfloat16
+
+    def __post_init__(self):
+        if self.k.dim() != 4 or self.k.shape != self.v.shape or {self.k.dtype, self.v.dtype} != {torch.float8_e4m3fn}:
+            raise ValueError("k and v must both be [n_pages, h_kv, page, dh] of float8_e4m3fn")
+        if any(e.shape != self.k.shape[:3] or e.dtype != torch.uint8 for e in (self.k_exp, self.v_exp)):
+            raise ValueError(f"k_exp and v_exp must be {list(self.k.shape[:3])} uint8")
+        if self.dtype not in _WDT:
+            raise ValueError("dtype must be bfloat16 or float32")
+        if len({t.device for t in (self.k, self.v, self.k_exp, self.v_exp)}) > 1:
+            raise ValueError("the cache's tensors must be on one device")
+        self.n_pages, self.h_kv, self.page, self.dh = self.k.shape
+        self.device = self.k.device.index
+        kv = sfn_kv(self.n_pages, self.page, self.h_kv, self.dh, _WDT[self.dtype], 0, _ptr(self.k, "k"), _ptr(self.v, "v"))
+        self.c = sfn_kv8(kv, _ptr(self.k_exp, "k_exp"), _ptr(self.v_exp, "v_exp"))
+        self.addr = ctypes.addressof(self.c)  # of the sfn_kv that it begins with, too
 
 
 @dataclass
@@ -397,6 +464,17 @@ class ResidualNorm:
         self.addr = ctypes.addressof(self.c)
 
 
+def _kind(kv, want):
+    # a handle of the other kind holds another structure, of smaller arrays
+    if not isinstance(kv, want):
+        raise TypeError(f"the cache must be a {want.__name__} (got {type(kv).__name__})")
+
+
+def _not_in_8_bits(kv):
+    if isinstance(kv, KVCache8):
+        raise TypeError("the cache is a KVCache8, which the kv8_cache calls take")
+
+
 def kv_cache_plan(kv: KVCache, held_len: torch.Tensor, ctx_len: torch.Tensor, new_len: torch.Tensor, table: torch.Tensor,
                   free_pages: torch.Tensor, n_free: torch.Tensor, n_free_out: torch.Tensor, cu: torch.Tensor,
                   kv_len: torch.Tensor, pos: torch.Tensor, slot: torch.Tensor, status: torch.Tensor, stream=None):
@@ -408,6 +486,7 @@ def kv_cache_plan(kv: KVCache, held_len: torch.Tensor, ctx_len: torch.Tensor, ne
 def kv_cache_append(kv: KVCache, k: torch.Tensor, v: torch.Tensor, slot: torch.Tensor, q: Optional[torch.Tensor] = None,
                     q_out: Optional[torch.Tensor] = None, pos: Optional[torch.Tensor] = None,
                     rope: Optional[torch.Tensor] = None, stream=None):
+    _not_in_8_bits(kv)
     st = _args.append(kv.addr, k, v, slot, q, q_out, pos, rope, _stream(stream))
     _check(st, "kv_cache_append")
 
@@ -419,9 +498,63 @@ def kv_cache_attend_workspace_size(kv: KVCache, R: int, T: int, h_q: int, max_ne
 def kv_cache_attend(kv: KVCache, q: torch.Tensor, table: torch.Tensor, cu: torch.Tensor, kv_len: torch.Tensor,
                     out: torch.Tensor, ws: torch.Tensor, max_new: int, max_len: int, scale: Optional[float] = None,
                     window: int = 0, stream=None):
+    _not_in_8_bits(kv)
     st = _args.attend(kv.addr, q, table, cu, kv_len, out, ws, max_new, max_len, kv.dh ** -0.5 if scale is None else scale,
                       window, _stream(stream))
     _check(st, "kv_cache_attend")
+
+
+def kv_cache_attend_shared_workspace_size(kv: KVCache, R: int, T: int, h_q: int, max_new: int, max_shared: int, max_own: int) -> int:
+    return int(_lib.kv_cache_attend_shared_workspace_size(kv.c, int(R), int(T), int(h_q), int(max_new), int(max_shared), int(max_own)))
+
+
+def kv_cache_attend_shared(kv: KVCache, q: torch.Tensor, prefix: torch.Tensor, shared_len: torch.Tensor, table: torch.Tensor,
+                           cu: torch.Tensor, kv_len: torch.Tensor, out: torch.Tensor, ws: torch.Tensor, max_new: int,
+                           max_shared: int, max_own: int, scale: Optional[float] = None, stream=None):
+    _kind(kv, KVCache)
+    st = _args.attend_shared(kv.addr, q, prefix, shared_len, table, cu, kv_len, out, ws, max_new, max_shared, max_own,
+                             kv.dh ** -0.5 if scale is None else scale, *_place(kv, stream))
+    _check(st, "kv_cache_attend_shared")
+
+
+def kv8_cache_append(kv: KVCache8, k: torch.Tensor, v: torch.Tensor, slot: torch.Tensor, q: Optional[torch.Tensor] = None,
+                     q_out: Optional[torch.Tensor] = None, pos: Optional[torch.Tensor] = None,
+                     rope: Optional[torch.Tensor] = None, stream=None):
+    _kind(kv, KVCache8)
+    st = _args.append8(kv.addr, k, v, slot, q, q_out, pos, rope, *_place(kv, stream))
+    _check(st, "kv8_cache_append")
+
+
+def kv8_cache_read(kv: KVCache8, slot: torch.Tensor, k_out: torch.Tensor, v_out: torch.Tensor, stream=None):
+    _kind(kv, KVCache8)
+    st = _args.read8(kv.addr, slot, k_out, v_out, *_place(kv, stream))
+    _check(st, "kv8_cache_read")
+
+
+def kv8_cache_attend_workspace_size(kv: KVCache8, R: int, T: int, h_q: int, max_new: int, max_len: int) -> int:
+    return int(_lib.kv8_cache_attend_workspace_size(kv.c, int(R), int(T), int(h_q), int(max_new), int(max_len)))
+
+
+def kv8_cache_attend(kv: KVCache8, q: torch.Tensor, table: torch.Tensor, cu: torch.Tensor, kv_len: torch.Tensor,
+                     out: torch.Tensor, ws: torch.Tensor, max_new: int, max_len: int, scale: Optional[float] = None,
+                     window: int = 0, stream=None):
+    _kind(kv, KVCache8)
+    st = _args.attend8(kv.addr, q, table, cu, kv_len, out, ws, max_new, max_len, kv.dh ** -0.5 if scale is None else scale,
+                       window, *_place(kv, stream))
+    _check(st, "kv8_cache_attend")
+
+
+def kv8_cache_attend_shared_workspace_size(kv: KVCache8, R: int, T: int, h_q: int, max_new: int, max_shared: int, max_own: int) -> int:
+    return int(_lib.kv8_cache_attend_shared_workspace_size(kv.c, int(R), int(T), int(h_q), int(max_new), int(max_shared), int(max_own)))
+
+
+def kv8_cache_attend_shared(kv: KVCache8, q: torch.Tensor, prefix: torch.Tensor, shared_len: torch.Tensor, table: torch.Tensor,
+                            cu: torch.Tensor, kv_len: torch.Tensor, out: torch.Tensor, ws: torch.Tensor, max_new: int,
+                            max_shared: int, max_own: int, scale: Optional[float] = None, stream=None):
+    _kind(kv, KVCache8)
+    st = _args.attend_shared8(kv.addr, q, prefix, shared_len, table, cu, kv_len, out, ws, max_new, max_shared, max_own,
+                              kv.dh ** -0.5 if scale is None else scale, *_place(kv, stream))
+    _check(st, "kv8_cache_attend_shared")
 
 
 def residual_norm(norm: ResidualNorm, h: torch.Tensor, y: Optional[torch.Tensor], h_out: Optional[torch.Tensor],

@@ -4,6 +4,7 @@
 
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdint>
@@ -392,6 +393,14 @@ int check_kv(const sfn_kv* kv, bool need_data) {
   return SFN_OK;
 }
 
+int check_kv8(const sfn_kv8* kv, bool need_data) {
+  if (!kv) return SFN_EINVAL;
+  const int st = check_kv(&kv->kv, need_data);
+  if (st != SFN_OK) return st;
+  if (need_data && (!kv->k_exp || !kv->v_exp)) return SFN_EINVAL;
+  return aligned16(kv->k_exp) && aligned16(kv->v_exp) ? SFN_OK : SFN_EALIGN;
+}
+
 int page_shift(int page) { return __builtin_ctz((unsigned)page); }
 
 // A token stride in elements: room for `heads` heads, 16-byte steps.
@@ -443,6 +452,26 @@ int kv_cache_plan(const sfn_kv* kv, int32_t R, int32_t max_pages, int32_t max_to
   }
 }
 
+namespace {
+
+// The arguments that both kinds of cache take alike.
+int check_append(const sfn_kv* kv, int32_t h_q, const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                 int64_t v_stride, const int32_t* pos, const int32_t* slot, const float* rope, int32_t n_pos, int32_t rot,
+                 const void* q_out) {
+  int st;
+  if ((h_q > 0) != (q != nullptr) || (h_q > 0) != (q_out != nullptr)) return SFN_EINVAL;
+  if (!k || !v || !slot) return SFN_EINVAL;
+  if (rope ? !pos : rot != 0) return SFN_EINVAL;
+  if (rope && (rot < 16 || rot > kv->dh || rot % 16 || n_pos < 1)) return SFN_ESHAPE;
+  if (h_q && (st = check_rows(q, q_stride, h_q, kv)) != SFN_OK) return st;
+  if ((st = check_rows(k, k_stride, kv->h_kv, kv)) != SFN_OK) return st;
+  if ((st = check_rows(v, v_stride, kv->h_kv, kv)) != SFN_OK) return st;
+  if (!aligned16(q_out) || !aligned16(rope) || !aligned4_or_null(pos) || !aligned4_or_null(slot)) return SFN_EALIGN;
+  return SFN_OK;
+}
+
+}  // namespace
+
 int kv_cache_append(const sfn_kv* kv, int32_t T, int32_t h_q, const void* q, int64_t q_stride, const void* k,
                     int64_t k_stride, const void* v, int64_t v_stride, const int32_t* pos, const int32_t* slot,
                     const float* rope, int32_t n_pos, int32_t rot, void* q_out, void* stream) {
@@ -451,14 +480,7 @@ int kv_cache_append(const sfn_kv* kv, int32_t T, int32_t h_q, const void* q, int
     if (st != SFN_OK) return st;
     if (T < 0 || T > SFN_MAX_STEP_TOKENS || h_q < 0 || h_q > SFN_MAX_HEADS) return SFN_ESHAPE;
     if (T == 0) return SFN_OK;  // empty arrays may have null addresses
-    if ((h_q > 0) != (q != nullptr) || (h_q > 0) != (q_out != nullptr)) return SFN_EINVAL;
-    if (!k || !v || !slot) return SFN_EINVAL;
-    if (rope ? !pos : rot != 0) return SFN_EINVAL;
-    if (rope && (rot < 16 || rot > kv->dh || rot % 16 || n_pos < 1)) return SFN_ESHAPE;
-    if (h_q && (st = check_rows(q, q_stride, h_q, kv)) != SFN_OK) return st;
-    if ((st = check_rows(k, k_stride, kv->h_kv, kv)) != SFN_OK) return st;
-    if ((st = check_rows(v, v_stride, kv->h_kv, kv)) != SFN_OK) return st;
-    if (!aligned16(q_out) || !aligned16(rope) || !aligned4_or_null(pos) || !aligned4_or_null(slot)) return SFN_EALIGN;
+    if ((st = check_append(kv, h_q, q, q_stride, k, k_stride, v, v_stride, pos, slot, rope, n_pos, rot, q_out)) != SFN_OK) return st;
     const int64_t e = wbytes(kv->dtype);
     sfn::KvAppendArgs a{};
     a.q = static_cast<const char*>(q);
@@ -487,11 +509,225 @@ int kv_cache_append(const sfn_kv* kv, int32_t T, int32_t h_q, const void* q, int
   }
 }
 
+int kv8_cache_append(const sfn_kv8* kv, int32_t T, int32_t h_q, const void* q, int64_t q_stride, const void* k,
+                     int64_t k_stride, const void* v, int64_t v_stride, const int32_t* pos, const int32_t* slot,
+                     const float* rope, int32_t n_pos, int32_t rot, void* q_out, void* stream) {
+  try {
+    int st = check_kv8(kv, true);
+    if (st != SFN_OK) return st;
+    if (T < 0 || T > SFN_MAX_STEP_TOKENS || h_q < 0 || h_q > SFN_MAX_HEADS) return SFN_ESHAPE;
+    if (T == 0) return SFN_OK;
+    const sfn_kv* c = &kv->kv;
+    if ((st = check_append(c, h_q, q, q_stride, k, k_stride, v, v_stride, pos, slot, rope, n_pos, rot, q_out)) != SFN_OK) return st;
+    const int64_t e = wbytes(c->dtype);
+    sfn::Kv8AppendArgs a{};
+    a.q = static_cast<const char*>(q);
+    a.k = static_cast<const char*>(k);
+    a.v = static_cast<const char*>(v);
+    a.q_stride = q_stride * e;
+    a.k_stride = k_stride * e;
+    a.v_stride = v_stride * e;
+    a.q_out = static_cast<char*>(q_out);
+    a.k_cache = static_cast<char*>(c->k);
+    a.v_cache = static_cast<char*>(c->v);
+    a.k_exp = kv->k_exp;
+    a.v_exp = kv->v_exp;
+    a.pos = pos;
+    a.slot = slot;
+    a.rope = rope;
+    a.T = T;
+    a.h_q = h_q;
+    a.h_kv = c->h_kv;
+    a.rot = rope ? rot : 0;
+    a.n_pos = n_pos;
+    a.n_pages = c->n_pages;
+    a.page_shift = page_shift(c->page);
+    return hip_status(sfn::launch_kv8_append(a, c->dh, c->dtype, static_cast<hipStream_t>(stream)));
+  } catch (...) {
+    return SFN_EHIP;
+  }
+}
+
+int kv8_cache_read(const sfn_kv8* kv, int32_t T, const int32_t* slot, void* k_out, int64_t k_stride, void* v_out,
+                   int64_t v_stride, void* stream) {
+  try {
+    int st = check_kv8(kv, true);
+    if (st != SFN_OK) return st;
+    if (T < 0 || T > SFN_MAX_STEP_TOKENS) return SFN_ESHAPE;
+    if (T == 0) return SFN_OK;
+    const sfn_kv* c = &kv->kv;
+    if (!slot || !k_out || !v_out) return SFN_EINVAL;
+    if ((st = check_rows(k_out, k_stride, c->h_kv, c)) != SFN_OK) return st;
+    if ((st = check_rows(v_out, v_stride, c->h_kv, c)) != SFN_OK) return st;
+    if (!aligned4_or_null(slot)) return SFN_EALIGN;
+    const int64_t e = wbytes(c->dtype);
+    sfn::Kv8ReadArgs a{};
+    a.k_cache = static_cast<const char*>(c->k);
+    a.v_cache = static_cast<const char*>(c->v);
+    a.k_exp = kv->k_exp;
+    a.v_exp = kv->v_exp;
+    a.slot = slot;
+    a.k_out = static_cast<char*>(k_out);
+    a.v_out = static_cast<char*>(v_out);
+    a.k_stride = k_stride * e;
+    a.v_stride = v_stride * e;
+    a.T = T;
+    a.h_kv = c->h_kv;
+    a.n_pages = c->n_pages;
+    a.page_shift = page_shift(c->page);
+    return hip_status(sfn::launch_kv8_read(a, c->dh, c->dtype, static_cast<hipStream_t>(stream)));
+  } catch (...) {
+    return SFN_EHIP;
+  }
+}
+
+namespace {
+
+size_t attend_size(const sfn_kv* kv, bool e4m3, int32_t R, int32_t T, int32_t h_q, int32_t max_new, int32_t max_len) {
+  if (check_attend(kv, R, T, h_q, max_new, max_len) != SFN_OK) return 0;
+  return attend_bytes(kv, sfn::attend_most_parts(R, h_q, kv->h_kv, kv->dtype, e4m3, max_new, max_len));
+}
+
+// What every attention launch has in common.
+sfn::AttendArgs attend_args(const sfn_kv* kv, const uint8_t* k_exp, const uint8_t* v_exp, int32_t T, int32_t h_q, const void* q,
+                            int64_t q_stride, const int32_t* cu, const int32_t* kv_len, float scale, void* out) {
+  sfn::AttendArgs a{};
+  a.k = static_cast<const char*>(kv->k);
+  a.v = static_cast<const char*>(kv->v);
+  a.k_exp = k_exp;
+  a.v_exp = v_exp;
+  a.q = static_cast<const char*>(q);
+  a.q_stride = q_stride * wbytes(kv->dtype);
+  a.cu = cu;
+  a.kv_len = kv_len;
+  a.out = static_cast<char*>(out);
+  a.T = T;
+  a.h_q = h_q;
+  a.h_kv = kv->h_kv;
+  a.g = h_q / kv->h_kv;
+  a.g_mul = ((1 << 21) + a.g - 1) / a.g;
+  a.page_shift = page_shift(kv->page);
+  a.n_pages = kv->n_pages;
+  a.scale_log2 = scale * 1.44269504088896340736f;
+  return a;
+}
+
+// Its division of the work, and where its parts lie: at w, as part_bytes(kv, p.parts) count them.
+void set_plan(sfn::AttendArgs& a, const sfn::AttendPlan& p, const sfn_kv* kv, char* w, int64_t parts) {
+  a.part_o = reinterpret_cast<float*>(w);
+  a.part_ml = reinterpret_cast<float*>(w + round256((size_t)parts * kv->dh * sizeof(float)));
+  a.tile_rows = p.tile_rows;
+  a.tile_keys = p.tile_keys;
+  a.row_tiles = p.row_tiles;
+  a.S = p.S;
+  a.chunk = p.chunk;
+}
+
+int attend(const sfn_kv* kv, const uint8_t* k_exp, const uint8_t* v_exp, int32_t R, int32_t T, int32_t h_q, const void* q, int64_t q_stride,
+           const int32_t* table, int32_t max_pages, const int32_t* cu, const int32_t* kv_len, int32_t max_new, int32_t max_len, float scale,
+           int32_t window, void* out, void* ws, size_t ws_bytes, void* stream) {
+  int st;
+  if ((st = check_attend(kv, R, T, h_q, max_new, max_len)) != SFN_OK) return st;
+  if (max_pages < 1) return SFN_ESHAPE;
+  if ((int64_t)max_pages * kv->page < max_len) max_len = max_pages * kv->page;
+  if (T == 0) return SFN_OK;
+  if (!q || !table || !cu || !kv_len || !out) return SFN_EINVAL;
+  if (!(scale > 0.0f) || !std::isfinite(scale) || window < 0) return SFN_EINVAL;
+  if ((st = check_rows(q, q_stride, h_q, kv)) != SFN_OK) return st;
+  if (!aligned16(out) || !aligned4_or_null(table) || !aligned4_or_null(cu) || !aligned4_or_null(kv_len)) return SFN_EALIGN;
+  if (window >= max_len) window = 0;  // every key is within it
+  const sfn::AttendPlan p = sfn::attend_plan(R, h_q, kv->h_kv, kv->dtype, k_exp != nullptr, max_new, max_len, window);
+  if ((int64_t)R * p.S * p.row_tiles * kv->h_kv > INT32_MAX) return SFN_ESHAPE;
+  if ((st = check_ws(ws, ws_bytes, attend_bytes(kv, p.parts))) != SFN_OK) return st;
+  sfn::AttendArgs a = attend_args(kv, k_exp, v_exp, T, h_q, q, q_stride, cu, kv_len, scale, out);
+  set_plan(a, p, kv, static_cast<char*>(ws) + sfn::kWsHeader, p.parts);
+  a.table = table;
+  a.max_pages = max_pages;
+  a.R = R;
+  a.max_new = max_new;
+  a.max_len = max_len;
+  a.window = window;
+  a.kind = sfn::ATTEND_PLAIN;
+  a.cu_step = 1;
+  a.whole = p.S == 1;
+  return hip_status(sfn::launch_kv_attend(a, kv->dh, kv->dtype, static_cast<hipStream_t>(stream)));
+}
+
+// Keys that a launch over the rest of the sequences may span: it begins with a whole tile.
+int32_t own_span(int32_t max_own) { return max_own + 64; }
+
+int check_shared(const sfn_kv* kv, int32_t R, int32_t T, int32_t h_q, int32_t max_new, int32_t max_shared, int32_t max_own) {
+  if (max_shared < 0 || max_own < 0 || (int64_t)max_shared + max_own > 1 << 30) return SFN_ESHAPE;
+  return check_attend(kv, R, T, h_q, max_new, max_shared + max_own);
+}
+
+// A launch's rows of parts in a call over a shared prefix: every row has at least one.
+int64_t shared_parts(int64_t rows, const sfn::AttendPlan& p) { return rows * p.S; }
+
+size_t shared_bytes(const sfn_kv* kv, int64_t own, int64_t prefix) {
+  return attend_bytes(kv, own) + attend_bytes(kv, prefix) - sfn::kWsHeader;
+}
+
+size_t shared_size(const sfn_kv* kv, bool e4m3, int32_t R, int32_t T, int32_t h_q, int32_t max_new, int32_t max_shared, int32_t max_own) {
+  if (check_shared(kv, R, T, h_q, max_new, max_shared, max_own) != SFN_OK) return 0;
+  const int32_t t = T > 0 ? T : 1;
+  const int64_t own = sfn::attend_most_parts(R, h_q, kv->h_kv, kv->dtype, e4m3, max_new, own_span(max_own));
+  const int64_t prefix = sfn::attend_most_parts(1, h_q, kv->h_kv, kv->dtype, e4m3, t, max_shared);
+  return shared_bytes(kv, std::max(own, (int64_t)R * max_new * h_q), std::max(prefix, (int64_t)t * h_q));
+}
+
+int attend_shared(const sfn_kv* kv, const uint8_t* k_exp, const uint8_t* v_exp, int32_t R, int32_t T, int32_t h_q, const void* q,
+                  int64_t q_stride, const int32_t* prefix, int32_t prefix_pages, const int32_t* shared_len, const int32_t* table,
+                  int32_t max_pages, const int32_t* cu, const int32_t* kv_len, int32_t max_new, int32_t max_shared, int32_t max_own,
+                  float scale, void* out, void* ws, size_t ws_bytes, void* stream) {
+  int st;
+  if ((st = check_shared(kv, R, T, h_q, max_new, max_shared, max_own)) != SFN_OK) return st;
+  if (max_pages < 1 || prefix_pages < 1) return SFN_ESHAPE;
+  if ((int64_t)prefix_pages * kv->page < max_shared) max_shared = prefix_pages * kv->page;
+  if (T == 0) return SFN_OK;
+  if (!q || !prefix || !shared_len || !table || !cu || !kv_len || !out) return SFN_EINVAL;
+  if (!(scale > 0.0f) || !std::isfinite(scale)) return SFN_EINVAL;
+  if ((st = check_rows(q, q_stride, h_q, kv)) != SFN_OK) return st;
+  if (!aligned16(out)) return SFN_EALIGN;
+  for (const int32_t* p : {prefix, shared_len, table, cu, kv_len})
+    if (!aligned4_or_null(p)) return SFN_EALIGN;
+  const bool e4m3 = k_exp != nullptr;
+  const sfn::AttendPlan po = sfn::attend_plan(R, h_q, kv->h_kv, kv->dtype, e4m3, max_new, own_span(max_own), 0);
+  const sfn::AttendPlan pp = sfn::attend_plan(1, h_q, kv->h_kv, kv->dtype, e4m3, T, max_shared, 0);
+  if ((int64_t)R * po.S * po.row_tiles * kv->h_kv > INT32_MAX || (int64_t)pp.S * pp.row_tiles * kv->h_kv > INT32_MAX) return SFN_ESHAPE;
+  const int64_t own_parts = shared_parts((int64_t)R * max_new * h_q, po), prefix_parts = shared_parts((int64_t)T * h_q, pp);
+  if ((st = check_ws(ws, ws_bytes, shared_bytes(kv, own_parts, prefix_parts))) != SFN_OK) return st;
+  char* const w = static_cast<char*>(ws) + sfn::kWsHeader;
+  sfn::AttendArgs a = attend_args(kv, k_exp, v_exp, T, h_q, q, q_stride, cu, kv_len, scale, out);
+  a.shared = shared_len;
+  a.max_shared = max_shared;
+  a.max_own = max_own;
+  sfn::AttendArgs b = a;
+  set_plan(a, po, kv, w, own_parts);
+  a.kind = sfn::ATTEND_OWN;
+  a.cu_step = 1;
+  a.table = table;
+  a.max_pages = max_pages;
+  a.R = R;
+  a.max_new = max_new;
+  a.max_len = (int32_t)std::min<int64_t>((int64_t)max_pages * kv->page, max_shared + max_own);
+  set_plan(b, pp, kv, w + (attend_bytes(kv, own_parts) - sfn::kWsHeader), prefix_parts);
+  b.kind = sfn::ATTEND_PREFIX;
+  b.cu_step = R;
+  b.table = prefix;
+  b.max_pages = prefix_pages;
+  b.R = 1;
+  b.max_new = T;
+  b.max_len = max_shared;
+  return hip_status(sfn::launch_kv_attend_shared(a, b, kv->dh, kv->dtype, static_cast<hipStream_t>(stream)));
+}
+
+}  // namespace
+
 size_t kv_cache_attend_workspace_size(const sfn_kv* kv, int32_t R, int32_t T, int32_t h_q, int32_t max_new,
                                       int32_t max_len) {
   try {
-    if (check_kv(kv, false) != SFN_OK || check_attend(kv, R, T, h_q, max_new, max_len) != SFN_OK) return 0;
-    return attend_bytes(kv, sfn::attend_most_parts(R, h_q, kv->h_kv, kv->dtype, max_new, max_len));
+    return check_kv(kv, false) == SFN_OK ? attend_size(kv, false, R, T, h_q, max_new, max_len) : 0;
   } catch (...) {
     return 0;
   }
@@ -502,51 +738,81 @@ int kv_cache_attend(const sfn_kv* kv, int32_t R, int32_t T, int32_t h_q, const v
                     int32_t max_new, int32_t max_len, float scale, int32_t window, void* out, void* ws,
                     size_t ws_bytes, void* stream) {
   try {
-    int st = check_kv(kv, true);
+    const int st = check_kv(kv, true);
     if (st != SFN_OK) return st;
-    if ((st = check_attend(kv, R, T, h_q, max_new, max_len)) != SFN_OK) return st;
-    if (max_pages < 1) return SFN_ESHAPE;
-    if ((int64_t)max_pages * kv->page < max_len) max_len = max_pages * kv->page;
-    if (T == 0) return SFN_OK;
-    if (!q || !table || !cu || !kv_len || !out) return SFN_EINVAL;
-    if (!(scale > 0.0f) || !std::isfinite(scale) || window < 0) return SFN_EINVAL;
-    if ((st = check_rows(q, q_stride, h_q, kv)) != SFN_OK) return st;
-    if (!aligned16(out) || !aligned4_or_null(table) || !aligned4_or_null(cu) || !aligned4_or_null(kv_len)) return SFN_EALIGN;
-    if (window >= max_len) window = 0;  // every key is within it
-    const sfn::AttendPlan p = sfn::attend_plan(R, h_q, kv->h_kv, kv->dtype, max_new, max_len, window);
-    if ((int64_t)R * p.S * p.row_tiles * kv->h_kv > INT32_MAX) return SFN_ESHAPE;
-    if ((st = check_ws(ws, ws_bytes, attend_bytes(kv, p.parts))) != SFN_OK) return st;
-    sfn::AttendArgs a{};
-    a.k = static_cast<const char*>(kv->k);
-    a.v = static_cast<const char*>(kv->v);
-    a.q = static_cast<const char*>(q);
-    a.q_stride = q_stride * wbytes(kv->dtype);
-    a.table = table;
-    a.cu = cu;
-    a.kv_len = kv_len;
-    a.out = static_cast<char*>(out);
-    char* w = static_cast<char*>(ws) + sfn::kWsHeader;
-    a.part_o = reinterpret_cast<float*>(w);
-    a.part_ml = reinterpret_cast<float*>(w + round256((size_t)p.parts * kv->dh * sizeof(float)));
-    a.R = R;
-    a.T = T;
-    a.h_q = h_q;
-    a.h_kv = kv->h_kv;
-    a.g = h_q / kv->h_kv;
-    a.g_mul = ((1 << 21) + a.g - 1) / a.g;
-    a.page_shift = page_shift(kv->page);
-    a.n_pages = kv->n_pages;
-    a.max_pages = max_pages;
-    a.max_new = max_new;
-    a.max_len = max_len;
-    a.window = window;
-    a.tile_rows = p.tile_rows;
-    a.tile_keys = p.tile_keys;
-    a.row_tiles = p.row_tiles;
-    a.S = p.S;
-    a.chunk = p.chunk;
-    a.scale_log2 = scale * 1.44269504088896340736f;
-    return hip_status(sfn::launch_kv_attend(a, kv->dh, kv->dtype, static_cast<hipStream_t>(stream)));
+    return attend(kv, nullptr, nullptr, R, T, h_q, q, q_stride, table, max_pages, cu, kv_len, max_new, max_len, scale, window, out, ws,
+                  ws_bytes, stream);
+  } catch (...) {
+    return SFN_EHIP;
+  }
+}
+
+size_t kv8_cache_attend_workspace_size(const sfn_kv8* kv, int32_t R, int32_t T, int32_t h_q, int32_t max_new,
+                                       int32_t max_len) {
+  try {
+    return check_kv8(kv, false) == SFN_OK ? attend_size(&kv->kv, true, R, T, h_q, max_new, max_len) : 0;
+  } catch (...) {
+    return 0;
+  }
+}
+
+int kv8_cache_attend(const sfn_kv8* kv, int32_t R, int32_t T, int32_t h_q, const void* q, int64_t q_stride,
+                     const int32_t* table, int32_t max_pages, const int32_t* cu, const int32_t* kv_len,
+                     int32_t max_new, int32_t max_len, float scale, int32_t window, void* out, void* ws,
+                     size_t ws_bytes, void* stream) {
+  try {
+    const int st = check_kv8(kv, true);
+    if (st != SFN_OK) return st;
+    return attend(&kv->kv, kv->k_exp, kv->v_exp, R, T, h_q, q, q_stride, table, max_pages, cu, kv_len, max_new, max_len, scale, window, out,
+                  ws, ws_bytes, stream);
+  } catch (...) {
+    return SFN_EHIP;
+  }
+}
+
+size_t kv_cache_attend_shared_workspace_size(const sfn_kv* kv, int32_t R, int32_t T, int32_t h_q, int32_t max_new,
+                                             int32_t max_shared, int32_t max_own) {
+  try {
+    return check_kv(kv, false) == SFN_OK ? shared_size(kv, false, R, T, h_q, max_new, max_shared, max_own) : 0;
+  } catch (...) {
+    return 0;
+  }
+}
+
+int kv_cache_attend_shared(const sfn_kv* kv, int32_t R, int32_t T, int32_t h_q, const void* q, int64_t q_stride,
+                           const int32_t* prefix, int32_t prefix_pages, const int32_t* shared_len,
+                           const int32_t* table, int32_t max_pages, const int32_t* cu, const int32_t* kv_len,
+                           int32_t max_new, int32_t max_shared, int32_t max_own, float scale, void* out, void* ws,
+                           size_t ws_bytes, void* stream) {
+  try {
+    const int st = check_kv(kv, true);
+    if (st != SFN_OK) return st;
+    return attend_shared(kv, nullptr, nullptr, R, T, h_q, q, q_stride, prefix, prefix_pages, shared_len, table, max_pages, cu, kv_len,
+                         max_new, max_shared, max_own, scale, out, ws, ws_bytes, stream);
+  } catch (...) {
+    return SFN_EHIP;
+  }
+}
+
+size_t kv8_cache_attend_shared_workspace_size(const sfn_kv8* kv, int32_t R, int32_t T, int32_t h_q, int32_t max_new,
+                                              int32_t max_shared, int32_t max_own) {
+  try {
+    return check_kv8(kv, false) == SFN_OK ? shared_size(&kv->kv, true, R, T, h_q, max_new, max_shared, max_own) : 0;
+  } catch (...) {
+    return 0;
+  }
+}
+
+int kv8_cache_attend_shared(const sfn_kv8* kv, int32_t R, int32_t T, int32_t h_q, const void* q, int64_t q_stride,
+                            const int32_t* prefix, int32_t prefix_pages, const int32_t* shared_len,
+                            const int32_t* table, int32_t max_pages, const int32_t* cu, const int32_t* kv_len,
+                            int32_t max_new, int32_t max_shared, int32_t max_own, float scale, void* out, void* ws,
+                            size_t ws_bytes, void* stream) {
+  try {
+    const int st = check_kv8(kv, true);
+    if (st != SFN_OK) return st;
+    return attend_shared(&kv->kv, kv->k_exp, kv->v_exp, R, T, h_q, q, q_stride, prefix, prefix_pages, shared_len, table, max_pages, cu,
+                         kv_len, max_new, max_shared, max_own, scale, out, ws, ws_bytes, stream);
   } catch (...) {
     return SFN_EHIP;
   }

@@ -114,14 +114,42 @@ struct KvAppendArgs {
 };
 hipError_t launch_kv_append(const KvAppendArgs& a, int dtype, hipStream_t stream);
 
+struct Kv8AppendArgs {
+  const char *q, *k, *v;
+  int64_t q_stride, k_stride, v_stride;  // bytes from token to token
+  char *q_out, *k_cache, *v_cache;
+  uint8_t *k_exp, *v_exp;
+  const int32_t *pos, *slot;
+  const float* rope;  // [n_pos, rot]
+  int T, h_q, h_kv, rot, n_pos, n_pages, page_shift;
+};
+hipError_t launch_kv8_append(const Kv8AppendArgs& a, int dh, int dtype, hipStream_t stream);
+
+struct Kv8ReadArgs {
+  const char *k_cache, *v_cache;
+  const uint8_t *k_exp, *v_exp;
+  const int32_t* slot;
+  char *k_out, *v_out;
+  int64_t k_stride, v_stride;  // bytes from token to token
+  int T, h_kv, n_pages, page_shift;
+};
+hipError_t launch_kv8_read(const Kv8ReadArgs& a, int dh, int dtype, hipStream_t stream);
+
+// What a launch attends to: each request's keys; a prefix that all tokens share, as one request
+// of them all; or each request's keys behind that prefix.
+enum { ATTEND_PLAIN = 0, ATTEND_PREFIX = 1, ATTEND_OWN = 2 };
 struct AttendArgs {
   const char *k, *v, *q;
+  const uint8_t *k_exp, *v_exp;  // the rows' powers of two of an 8-bit cache, else null
   int64_t q_stride;  // bytes from token to token
-  const int32_t *table, *cu, *kv_len;
+  const int32_t *table, *cu, *kv_len, *shared;
   char* out;
   float *part_o, *part_ml;  // [R, max_new, h_q, S, dh] and [R, max_new, h_q, S, 2] (S > 1)
   int R, T, h_q, h_kv, g, g_mul, page_shift, n_pages, max_pages, max_new, max_len, window;
+  int kind, cu_step;          // request r's tokens are [cu[r], cu[r + cu_step])
+  int max_shared, max_own;    // of ATTEND_OWN
   int tile_rows, tile_keys, row_tiles, S, chunk;  // see AttendPlan
+  int whole;                                      // results, and not parts to join, are written
   float scale_log2;                               // score scale times log2(e)
 };  // g = h_q / h_kv, g_mul = ceil(2^21 / g)
 struct AttendPlan {
@@ -129,10 +157,11 @@ struct AttendPlan {
   int row_tiles, S, chunk;   // workgroups for a key head's rows and for its keys, keys of a split
   int64_t parts;             // rows of partial results
 };
-AttendPlan attend_plan(int R, int h_q, int h_kv, int dtype, int max_new, int max_len, int window);
+AttendPlan attend_plan(int R, int h_q, int h_kv, int dtype, bool e4m3, int max_new, int max_len, int window);
 // Rows of partial results that no call within these bounds passes.
-int64_t attend_most_parts(int R, int h_q, int h_kv, int dtype, int max_new, int max_len);
+int64_t attend_most_parts(int R, int h_q, int h_kv, int dtype, bool e4m3, int max_new, int max_len);
 hipError_t launch_kv_attend(const AttendArgs& a, int dh, int dtype, hipStream_t stream);
+hipError_t launch_kv_attend_shared(const AttendArgs& own, const AttendArgs& prefix, int dh, int dtype, hipStream_t stream);
 
 struct NormArgs {
   const char *h, *y, *w_post, *w_pre, *gate;

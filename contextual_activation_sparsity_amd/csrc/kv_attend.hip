@@ -1,7 +1,9 @@
 // Attention of each request's new tokens over its pages of the key/value cache.
 
 #include <algorithm>
+#include <type_traits>
 
+#include "cache8.h"
 #include "kernels.h"
 #include "serving_common.h"
 #include "sparse_ffn.h"
@@ -14,6 +16,36 @@ typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8_t;
 
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr int kMaxSplits = 256;  // the join kernel's threads
+
+// What the cache holds: values of the tokens' type, or e4m3 codes and a power of two to a row.
+enum { CT_SAME = 0, CT_E4M3 = 1 };
+
+// One request of a call: its tokens are [t0, t0 + n), the first of them stands at position
+// `past`, and the call reads its keys [from, len). Of a call over a shared prefix, the part over
+// the prefix takes all tokens as one request, all of which see every key of it (past = len);
+// the part over the rest starts behind the prefix for a request whose tokens all come after it,
+// and otherwise reads everything from the request's own pages.
+struct Request {
+  int t0, n, len, past, from;
+  __device__ __forceinline__ Request(const AttendArgs& a, int r) {
+    t0 = min(max(gp(a.cu)[r], 0), a.T);
+    n = min(max(gp(a.cu)[r + a.cu_step], t0), a.T) - t0;
+    from = 0;
+    if (a.kind == ATTEND_PREFIX) {
+      past = len = min(max(gp(a.shared)[0], 0), a.max_len);
+      return;
+    }
+    len = min(max(gp(a.kv_len)[r], 0), a.max_len);
+    if (a.kind == ATTEND_OWN) {
+      const int shared = shared_len(a);
+      len = min(len, shared + a.max_own);
+      if (len - n >= shared) from = shared;
+      else len = min(len, a.max_own);
+    }
+    past = len - n;
+  }
+  __device__ __forceinline__ static int shared_len(const AttendArgs& a) { return min(max(gp(a.shared)[0], 0), a.max_shared); }
+};
 
 // ---- split attention -----------------------------------------------------------------
 //
@@ -47,16 +79,23 @@ constexpr int kMaxSplits = 256;  // the join kernel's threads
 // fp32 with more rows reads K and V again for every tile of 32, and is bound by the products,
 // which wait for each tile's loads: two requests of 1000 tokens after 4000 others, 32 / 8 heads
 // of 128, 1387 us, 106 TFLOP/s where an fp32 product of 8192 x 8192 reaches 154.
-template <int WT, int DH>
+template <int WT, int CT, int DH>
 struct AttnTile {
-  static constexpr bool kBf = WT == WT_BF16;
+  static constexpr bool kBf = WT == WT_BF16, k8 = CT == CT_E4M3;
   static constexpr int KB = kBf ? 2 : 4;           // bytes of a value
-  static constexpr int KT = kBf ? 32 : 16;         // keys of a tile
+  static constexpr int CB = k8 ? 1 : KB;           // and in the cache
+  static constexpr int KT = (kBf ? 32 : 16) * (k8 ? 2 : 1);  // keys of a tile
   static constexpr int NG = KT / 16;               // 16-key groups (each within a page)
   static constexpr int NQ = DH * KB / 64;          // 16-byte chunks a lane holds of a row (K, Q)
-  static constexpr int VW = kBf && DH == 128 ? 8 : 4;  // values a lane reads of a V row
+  static constexpr int VW = (kBf || k8) && DH == 128 ? 8 : 4;  // values a lane reads of a V row
   static constexpr int NB = DH / (16 * VW);        // times that
   static constexpr int NO = DH / 16;               // output blocks
+  // Where in its row chunk s of lane quarter q starts (values). The order of the contracted
+  // values is free, so a lane takes 16 codes at once and the chunks that they make follow.
+  __device__ __forceinline__ static int chunk_at(int s, int q) {
+    constexpr int E = 16 / KB, NC = k8 ? 16 / E : 1;
+    return k8 ? 64 * (s / NC) + 16 * q + E * (s % NC) : 4 * E * s + E * q;
+  }
 };
 
 // Values d4 .. d4 + 3 of one output row, from their unscaled sums and the sum of weights.
@@ -96,9 +135,10 @@ __device__ __forceinline__ float add_pair(uint32_t w, float sum) {
 // its weights (group, key 4q + i); l += the lane's weights.
 template <int WT, int DH>
 __device__ __forceinline__ void add_weighted(
-    const uint32_t (&v)[AttnTile<WT, DH>::NG][4][AttnTile<WT, DH>::NB][AttnTile<WT, DH>::VW * AttnTile<WT, DH>::KB / 4],
-    const f32x4_t (&p)[AttnTile<WT, DH>::NG], f32x4_t (&acc)[AttnTile<WT, DH>::NO], float& l) {
-  using C = AttnTile<WT, DH>;
+    const uint32_t (&v)[AttnTile<WT, CT_SAME, DH>::NG][4][AttnTile<WT, CT_SAME, DH>::NB]
+                       [AttnTile<WT, CT_SAME, DH>::VW * AttnTile<WT, CT_SAME, DH>::KB / 4],
+    const f32x4_t (&p)[AttnTile<WT, CT_SAME, DH>::NG], f32x4_t (&acc)[AttnTile<WT, CT_SAME, DH>::NO], float& l) {
+  using C = AttnTile<WT, CT_SAME, DH>;
   if constexpr (C::kBf) {
     // the weights are rounded to bf16, as V is: the matrix cores take both operands in one
     // type, and the rounding (at most 2^-8 of each weight, of either sign) adds no more to
@@ -134,10 +174,10 @@ __device__ __forceinline__ void add_weighted(
 
 // The same for the values of key kk that are not finite, and only into the rows that see
 // it. vp: the lane's first value of that key's row.
-template <int WT, int DH>
-__device__ __forceinline__ void add_one_key(const SFN_GLOBAL char* vp, const f32x4_t (&p)[AttnTile<WT, DH>::NG], int kk, int q,
-                                            bool sees, f32x4_t (&acc)[AttnTile<WT, DH>::NO]) {
-  using C = AttnTile<WT, DH>;
+template <int WT, int CT, int DH>
+__device__ __forceinline__ void add_one_key(const SFN_GLOBAL char* vp, const f32x4_t (&p)[AttnTile<WT, CT, DH>::NG], int kk, int q,
+                                            bool sees, f32x4_t (&acc)[AttnTile<WT, CT, DH>::NO]) {
+  using C = AttnTile<WT, CT, DH>;
   float w = 0.f;  // the weight, in the lanes that hold the key
 #pragma unroll
   for (int u = 0; u < C::NG; ++u)
@@ -150,8 +190,10 @@ __device__ __forceinline__ void add_one_key(const SFN_GLOBAL char* vp, const f32
 #pragma unroll
     for (int e = 0; e < C::VW; ++e) {
       // the key's value goes through the products as operand element 0
-      uint32_t x = C::kBf ? reinterpret_cast<const SFN_GLOBAL uint16_t*>(vp)[nb * 16 * C::VW + e]
-                          : reinterpret_cast<const SFN_GLOBAL uint32_t*>(vp)[nb * 16 * C::VW + e];
+      uint32_t x;
+      if constexpr (C::k8) x = not_a_number(vp[nb * 16 * C::VW + e]) ? (C::kBf ? 0x7fc0u : 0x7fc00000u) : 0u;
+      else if constexpr (C::kBf) x = reinterpret_cast<const SFN_GLOBAL uint16_t*>(vp)[nb * 16 * C::VW + e];
+      else x = reinterpret_cast<const SFN_GLOBAL uint32_t*>(vp)[nb * 16 * C::VW + e];
       x = mine && not_finite<WT>(x) ? x : 0u;
       f32x4_t& o = acc[nb * C::VW + e];
       f32x4_t t;
@@ -168,9 +210,9 @@ __device__ __forceinline__ void add_one_key(const SFN_GLOBAL char* vp, const f32
 }
 
 // One tile of keys in a lane's registers.
-template <int WT, int DH>
+template <int WT, int CT, int DH>
 struct KeyTile {
-  using C = AttnTile<WT, DH>;
+  using C = AttnTile<WT, CT, DH>;
   uint4 k[C::NG][C::NQ];
   uint32_t v[C::NG][4][C::NB][C::VW * C::KB / 4];
 
@@ -204,6 +246,12 @@ struct KeyTile {
           }
         }
     }
+  }
+
+  // Chunk i of the key's row in group u.
+  __device__ __forceinline__ uint4 key_chunk(int u, int i) const { return k[u][i]; }
+  __device__ __forceinline__ void add_values(const f32x4_t (&p)[C::NG], f32x4_t (&acc)[C::NO], float& l) const {
+    add_weighted<WT, DH>(v, p, acc, l);
   }
 
   // Zeroes the values of keys from `keys` on (keys of the tile that the sequence has); returns
@@ -242,6 +290,127 @@ struct KeyTile {
   }
 };
 
+// The same of an 8-bit cache: the codes and their rows' bytes, turned into values of the tokens'
+// type as they go into the products, keys and values times their row's power of two (exact in
+// bf16: four bits of significand).
+template <int WT, int DH>
+struct KeyTile<WT, CT_E4M3, DH> {
+  using C = AttnTile<WT, CT_E4M3, DH>;
+  static constexpr int NR = DH / 64, NV = C::VW / 4;  // 16-byte loads of a K row, words of a V row
+  uint4 k[C::NG][NR];
+  uint32_t v[C::NG][4][NV];
+  uint32_t kb[C::NG], vb[C::NG];  // the bytes of key c, and of keys 4q .. 4q + 3
+
+  __device__ __forceinline__ void load(const AttendArgs& a, const int64_t (&row)[C::NG], int c, int q) {
+#pragma unroll
+    for (int u = 0; u < C::NG; ++u) {
+      const SFN_GLOBAL char* kp = gp(a.k) + (row[u] + c) * DH + 16 * q;
+#pragma unroll
+      for (int s = 0; s < NR; ++s) k[u][s] = ldg16(kp + 64 * s);
+      kb[u] = gp(a.k_exp)[row[u] + c];
+    }
+#pragma unroll
+    for (int u = 0; u < C::NG; ++u) {
+      const SFN_GLOBAL char* vp = gp(a.v) + (row[u] + 4 * q) * DH + c * C::VW;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if constexpr (NV == 2) {
+          const uint64_t w = __builtin_nontemporal_load(reinterpret_cast<const SFN_GLOBAL uint64_t*>(vp + j * DH));
+          v[u][j][0] = (uint32_t)w;
+          v[u][j][1] = (uint32_t)(w >> 32);
+        } else {
+          v[u][j][0] = __builtin_nontemporal_load(reinterpret_cast<const SFN_GLOBAL uint32_t*>(vp + j * DH));
+        }
+      }
+      vb[u] = *reinterpret_cast<const SFN_GLOBAL uint32_t*>(gp(a.v_exp) + row[u] + 4 * q);
+    }
+  }
+
+  __device__ __forceinline__ uint4 key_chunk(int u, int i) const {
+    const float scale = scale_of(kb[u]);
+    if constexpr (C::kBf) {
+      const uint4 w = k[u][i >> 1];
+      const uint32_t a = i & 1 ? w.z : w.x, b = i & 1 ? w.w : w.y;
+      return make_uint4(pair_of<false>(a, scale), pair_of<true>(a, scale), pair_of<false>(b, scale), pair_of<true>(b, scale));
+    } else {
+      const uint4 w = k[u][i >> 2];
+      float f[4];
+      values_of((i & 3) == 0 ? w.x : (i & 3) == 1 ? w.y : (i & 3) == 2 ? w.z : w.w, scale, f);
+      return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+    }
+  }
+
+  __device__ __forceinline__ void add_values(const f32x4_t (&p)[C::NG], f32x4_t (&acc)[C::NO], float& l) const {
+    float scale[C::NG][4];
+#pragma unroll
+    for (int u = 0; u < C::NG; ++u)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) scale[u][j] = scale_of(vb[u] >> (8 * j) & 0xffu);
+    if constexpr (C::kBf) {
+#pragma unroll
+      for (int u = 0; u < C::NG; u += 2) {
+        // rounded to bf16, and their sum, as in add_weighted
+        const uint4 pw = make_uint4(pack_bf16(p[u][0], p[u][1]), pack_bf16(p[u][2], p[u][3]), pack_bf16(p[u + 1][0], p[u + 1][1]),
+                                    pack_bf16(p[u + 1][2], p[u + 1][3]));
+        l = add_pair(pw.x, add_pair(pw.y, l)) + add_pair(pw.z, add_pair(pw.w, 0.f));
+#pragma unroll
+        for (int e = 0; e < C::VW; e += 2) {
+          uint32_t x[2][4];  // values e and e + 1 of the lane's eight keys
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              x[h][j] = e & 2 ? pair_of<true>(v[u + h][j][e >> 2], scale[u + h][j]) : pair_of<false>(v[u + h][j][e >> 2], scale[u + h][j]);
+#pragma unroll
+          for (int o = 0; o < 2; ++o) {
+            const uint32_t sel = o ? 0x07060302u : 0x05040100u;
+            const uint4 w = make_uint4(__builtin_amdgcn_perm(x[0][1], x[0][0], sel), __builtin_amdgcn_perm(x[0][3], x[0][2], sel),
+                                       __builtin_amdgcn_perm(x[1][1], x[1][0], sel), __builtin_amdgcn_perm(x[1][3], x[1][2], sel));
+            acc[e + o] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, w), __builtin_bit_cast(bf16x8_t, pw),
+                                                                 acc[e + o], 0, 0, 0);
+          }
+        }
+      }
+    } else {
+#pragma unroll
+      for (int u = 0; u < C::NG; ++u) {
+        l += (p[u][0] + p[u][1]) + (p[u][2] + p[u][3]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int e = 0; e < C::VW; e += 4) {
+            float f[4];
+            values_of(v[u][j][e >> 2], scale[u][j], f);
+#pragma unroll
+            for (int o = 0; o < 4; ++o) acc[e + o] = __builtin_amdgcn_mfma_f32_16x16x4f32(f[o], p[u][j], acc[e + o], 0, 0, 0);
+          }
+      }
+    }
+  }
+
+  __device__ __forceinline__ bool clean(int keys, int q) {
+    uint32_t odd = 0;
+#pragma unroll
+    for (int u = 0; u < C::NG; ++u)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int w = 0; w < NV; ++w) {
+          uint32_t& x = v[u][j][w];
+          x = 16 * u + j < keys - 4 * q ? x : 0u;
+          odd |= nan_codes(x);
+        }
+    if (!__any(odd != 0)) return false;
+#pragma unroll
+    for (int u = 0; u < C::NG; ++u)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int w = 0; w < NV; ++w) v[u][j][w] = without_nan(v[u][j][w]);
+    return true;
+  }
+};
+
 // The rows of a tile that starts at row rho0: which token and which of the g heads.
 struct RowMap {
   int tok0, rem0, mul, g;
@@ -254,9 +423,9 @@ struct RowMap {
   __device__ __forceinline__ int head(int i, int tok) const { return i + rem0 - (tok - tok0) * g; }
 };
 
-template <int WT, int DH, int RT, int NW>
+template <int WT, int CT, int DH, int RT, int NW>
 __global__ __launch_bounds__(64 * NW, NW == 8 || RT == 2 ? 2 : 3) void attend_split_kernel(AttendArgs a) {
-  using C = AttnTile<WT, DH>;
+  using C = AttnTile<WT, CT, DH>;
   constexpr int KT = C::KT, NG = C::NG, NQ = C::NQ, VW = C::VW, NB = C::NB, NO = C::NO, KB = C::KB;
   constexpr int TR = 16 * RT, ROW = DH * KB;
   __shared__ float s_m[NW][TR], s_l[NW][TR];
@@ -279,24 +448,23 @@ __global__ __launch_bounds__(64 * NW, NW == 8 || RT == 2 ? 2 : 3) void attend_sp
 #pragma unroll
   for (int u = 0; u < NG; ++u) page[u] = page_of(split * a.chunk + wave * KT + 16 * u);
 
-  const int t0 = min(max(gp(a.cu)[r], 0), a.T), t1 = min(max(gp(a.cu)[r + 1], t0), a.T);
-  const int n = t1 - t0, g = a.g, rows = min(n, a.max_new) * g;
-  const int len = min(max(gp(a.kv_len)[r], 0), a.max_len);
+  const Request req(a, r);
+  const int t0 = req.t0, len = req.len, past = req.past;
+  const int g = a.g, rows = min(req.n, a.max_new) * g;
   const int rho0 = rtile * TR;
   if (rho0 >= rows) return;
-  const int past = len - n;  // position of the first new token
   const RowMap map(a, rho0);
   const int last = min(TR, rows - rho0) - 1, tok1 = map.token(last);
   // keys that some row of the tile sees, and that every row sees
   const int hi = max(0, min(past + tok1 + 1, len));
-  const int lo = a.window > 0 ? max(0, past + map.tok0 + 1 - a.window) : 0;
+  const int lo = a.window > 0 ? max(0, past + map.tok0 + 1 - a.window) : req.from;
   const int hi_all = min(past + map.tok0 + 1, len);
-  const int lo_all = a.window > 0 ? max(0, past + tok1 + 1 - a.window) : 0;
+  const int lo_all = a.window > 0 ? max(0, past + tok1 + 1 - a.window) : req.from;
   const int k0 = (lo & ~(KT - 1)) + split * a.chunk, k1 = min(k0 + a.chunk, hi);
   if (split > 0 && k0 >= hi) return;
 
   const int kw = k0 + wave * KT;
-  KeyTile<WT, DH> tile;
+  KeyTile<WT, CT, DH> tile;
   auto find = [&](int kt) {
 #pragma unroll
     for (int u = 0; u < NG; ++u) page[u] = page_of(kt + 16 * u);
@@ -321,11 +489,11 @@ __global__ __launch_bounds__(64 * NW, NW == 8 || RT == 2 ? 2 : 3) void attend_sp
   for (int x = 0; x < RT; ++x) {
     const bool ok = 16 * x + c <= last;
     const int i = ok ? 16 * x + c : 0, tok = map.token(i), head = hk * g + map.head(i, tok);
-    const SFN_GLOBAL char* src = gp(a.q) + (int64_t)(t0 + tok) * a.q_stride + head * ROW + 16 * q;
+    const SFN_GLOBAL char* src = gp(a.q) + (int64_t)(t0 + tok) * a.q_stride + head * ROW;
 #pragma unroll
-    for (int s = 0; s < NQ; ++s) qf[x][s] = ld16(src + 64 * s);
+    for (int s = 0; s < NQ; ++s) qf[x][s] = ld16(src + C::chunk_at(s, q) * KB);
     row_hi[x] = ok ? min(past + tok + 1, len) : 0;
-    row_lo[x] = a.window > 0 ? past + tok + 1 - a.window : 0;
+    row_lo[x] = a.window > 0 ? past + tok + 1 - a.window : req.from;
   }
 
   f32x4_t acc[RT][NO];
@@ -354,7 +522,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 || RT == 2 ? 2 : 3) void attend_sp
           s[u] = zero;
 #pragma unroll
           for (int i = 0; i < NQ; ++i)
-            s[u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, tile.k[u][i]),
+            s[u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, tile.key_chunk(u, i)),
                                                            __builtin_bit_cast(bf16x8_t, qf[x][i]), s[u], 0, 0, 0);
         } else {
           // four sums side by side: half the rounding error of one chain of dh additions (sharp
@@ -363,7 +531,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 || RT == 2 ? 2 : 3) void attend_sp
           f32x4_t part[4] = {zero, zero, zero, zero};
 #pragma unroll
           for (int i = 0; i < NQ; ++i) {
-            const f32x4_t kk = __builtin_bit_cast(f32x4_t, tile.k[u][i]), qq = __builtin_bit_cast(f32x4_t, qf[x][i]);
+            const f32x4_t kk = __builtin_bit_cast(f32x4_t, tile.key_chunk(u, i)), qq = __builtin_bit_cast(f32x4_t, qf[x][i]);
 #pragma unroll
             for (int e = 0; e < 4; ++e) part[e] = __builtin_amdgcn_mfma_f32_16x16x4f32(kk[e], qq[e], part[e], 0, 0, 0);
           }
@@ -399,13 +567,13 @@ __global__ __launch_bounds__(64 * NW, NW == 8 || RT == 2 ? 2 : 3) void attend_sp
       for (int u = 0; u < NG; ++u)
 #pragma unroll
         for (int i = 0; i < 4; ++i) s[u][i] = exp2_f(fmaf(s[u][i], a.scale_log2, -ms));
-      add_weighted<WT, DH>(tile.v, s, acc[x], l[x]);
+      tile.add_values(s, acc[x], l[x]);
       if (odd) {
         // the values that are not finite: key by key, read again, into the rows that see them
 #pragma unroll 1
         for (int kk = 0; kk < KT && kt + kk < len; ++kk)
-          add_one_key<WT, DH>(gp(a.v) + (row_in(page_of(kt + kk), kt + kk) + (kk & 15)) * ROW + c * VW * KB, s, kk, q,
-                              kt + kk < row_hi[x] && kt + kk >= row_lo[x], acc[x]);
+          add_one_key<WT, CT, DH>(gp(a.v) + ((row_in(page_of(kt + kk), kt + kk) + (kk & 15)) * DH + c * VW) * C::CB, s, kk, q,
+                                  kt + kk < row_hi[x] && kt + kk >= row_lo[x], acc[x]);
       }
     }
     kt += NW * KT;
@@ -448,7 +616,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 || RT == 2 ? 2 : 3) void attend_sp
       L += s_l[w][x];
       o += *reinterpret_cast<const f32x4_t*>(&s_o[w][x][d4]);
     }
-    if (a.S == 1) {
+    if (a.whole) {
       store_row<WT, DH>(a, t0 + tok, head, d4, o, L);
     } else {
       const int64_t at = (((int64_t)r * a.max_new + tok) * a.h_q + head) * a.S + split;
@@ -516,7 +684,7 @@ __device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t from, uint32_
 }
 
 // One wave's state over its 32 rows, and where its lanes read and load.
-template <int DH>
+template <int CT, int DH>
 struct TileWave {
   static constexpr int ROW = DH * 2;           // bytes of a row
   static constexpr int NC = DH / 8;            // 16-byte chunks of a row
@@ -588,10 +756,14 @@ struct TileWave {
       for (int d = 0; d < ND; ++d)
 #pragma unroll
         for (int i = 0; i < 16; i += 4) {
-          const uint64_t x4 = *reinterpret_cast<const SFN_GLOBAL uint64_t*>(v + 64 * d + 4 * i + first);  // of acc[d][i .. i + 3]
+          uint64_t x4;  // of acc[d][i .. i + 3]
+          if constexpr (CT == CT_E4M3) x4 = *reinterpret_cast<const SFN_GLOBAL uint32_t*>(v + (64 * d + 4 * i + first) / 2);
+          else x4 = *reinterpret_cast<const SFN_GLOBAL uint64_t*>(v + 64 * d + 4 * i + first);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const uint32_t x = (uint32_t)(x4 >> (16 * e)) << 16;
+            uint32_t x;
+            if constexpr (CT == CT_E4M3) x = not_a_number((uint32_t)(x4 >> (8 * e))) ? 0x7fc00000u : 0u;
+            else x = (uint32_t)(x4 >> (16 * e)) << 16;
             acc[d][i + e] = sees && not_finite<WT_F32>(x) ? fmaf(p, __uint_as_float(x), acc[d][i + e]) : acc[d][i + e];
           }
         }
@@ -663,12 +835,46 @@ struct TileWave {
   }
 };
 
+// Of an 8-bit cache: a wave's 16 rows of a stage of K or of V on their way through registers. They
+// are read while the products of the stage before are under way, turned into bf16 and written to
+// LDS after them, so that the products read the same stages as above.
+template <int DH>
+struct CodeRows {
+  static constexpr int LR = DH / 16, RI = 64 / LR, N = 16 / RI;  // lanes of a row, rows of one load, loads
+  uint4 w[N];
+  uint32_t b[N];
+  __device__ __forceinline__ void load(const SFN_GLOBAL char* rows, const SFN_GLOBAL uint8_t* exps, int lane) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int row = i * RI + lane / LR;
+      w[i] = ld16(rows + row * DH + (lane % LR) * 16);
+      b[i] = exps[row];
+    }
+  }
+  // place(row, ch): where chunk ch (8 values) of a row lies; to: the wave's part of the stage
+  template <class Place>
+  __device__ __forceinline__ void put(SFN_LDS char* to, int lane, Place place) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int row = i * RI + lane / LR, ch = (lane % LR) * 2;
+      const float s = scale_of(b[i]);
+      const uint4 x = w[i];
+      *reinterpret_cast<SFN_LDS u32x4_t*>(to + row * DH * 2 + place(row, ch) * 16) =
+          u32x4_t{pair_of<false>(x.x, s), pair_of<true>(x.x, s), pair_of<false>(x.y, s), pair_of<true>(x.y, s)};
+      *reinterpret_cast<SFN_LDS u32x4_t*>(to + row * DH * 2 + place(row, ch + 1) * 16) =
+          u32x4_t{pair_of<false>(x.z, s), pair_of<true>(x.z, s), pair_of<false>(x.w, s), pair_of<true>(x.w, s)};
+    }
+  }
+};
+
 // KG groups of four waves: with two of them (a split of the keys for few row tiles) each takes
 // every second stage, with buffers of its own, and the groups join in LDS at the end, so that
 // there are half as many parts to write and join as with two workgroups.
-template <int DH, int KG>
+template <int CT, int DH, int KG>
 __global__ __launch_bounds__(256 * KG, 2) void attend_tile_kernel(AttendArgs a) {
-  using W = TileWave<DH>;
+  using W = TileWave<CT, DH>;
+  constexpr bool k8 = CT == CT_E4M3;
+  constexpr int CROW = k8 ? DH : DH * 2;  // bytes of a row in the cache
   constexpr int ND = W::ND, NC = W::NC, ROW = W::ROW, KT = kTileKeys;
   constexpr int STAGE = KT * ROW;  // bytes of a stage of K, and of V
   // two arrays, so that the compiler knows that the reads of one need not wait for the loads
@@ -684,53 +890,66 @@ __global__ __launch_bounds__(256 * KG, 2) void attend_tile_kernel(AttendArgs a) 
   const int rtile = a.row_tiles == 1 ? 0 : a.row_tiles - 1 - blockIdx.x / a.h_kv;  // the longest first
   const int split = blockIdx.y, r = blockIdx.z;
 
-  // byte offset in the cache of this wave's 16 rows of the stage at kt (one group of keys, in
+  // the first in the cache of this wave's 16 rows of the stage at kt (one group of keys, in
   // one page; past the sequence any page of the cache)
   const int lg = a.page_shift, pm = (1 << lg) - 1;
   const SFN_GLOBAL int32_t* table = gp(a.table) + (int64_t)r * a.max_pages;
   auto page_of = [&](int kt) { return __builtin_amdgcn_readfirstlane(table[min((kt + 16 * wave) >> lg, a.max_pages - 1)]); };
   auto rows_in = [&](int page, int kt) -> int64_t {
-    return ((((int64_t)min(max(page, 0), a.n_pages - 1) * a.h_kv + hk) << lg) + ((kt + 16 * wave) & pm)) * ROW;
+    return (((int64_t)min(max(page, 0), a.n_pages - 1) * a.h_kv + hk) << lg) + ((kt + 16 * wave) & pm);
   };
   // without a window the first stage does not depend on the lengths: its page is read with them
   int page = page_of(split * a.chunk + kg * KT);
 
-  const int t0 = min(max(gp(a.cu)[r], 0), a.T), t1 = min(max(gp(a.cu)[r + 1], t0), a.T);
-  const int n = t1 - t0, g = a.g, rows = min(n, a.max_new) * g;
-  const int len = min(max(gp(a.kv_len)[r], 0), a.max_len);
+  const Request req(a, r);
+  const int t0 = req.t0, len = req.len, past = req.past;
+  const int g = a.g, rows = min(req.n, a.max_new) * g;
   const int rho0 = rtile * kTileRows;
   if (rho0 >= rows) return;
-  const int past = len - n;
   const RowMap map(a, rho0);
   const int last = min(kTileRows, rows - rho0) - 1;  // the tile's last row
   // keys that some row of the tile sees, and that every row sees
   const int tok1 = map.token(last);
   const int hi = max(0, min(past + tok1 + 1, len));
-  const int lo = a.window > 0 ? max(0, past + map.tok0 + 1 - a.window) : 0;
+  const int lo = a.window > 0 ? max(0, past + map.tok0 + 1 - a.window) : req.from;
   const int tile_hi = min(past + map.tok0 + 1, len);
-  const int tile_lo = a.window > 0 ? past + tok1 + 1 - a.window : 0;
+  const int tile_lo = a.window > 0 ? past + tok1 + 1 - a.window : req.from;
   const int k0 = (lo & ~(KT - 1)) + split * a.chunk, k1 = min(k0 + a.chunk, hi);
   if (split > 0 && k0 >= hi) return;
 
   const int group = kg * 2 * STAGE, mine = group + 16 * wave * ROW;
   const int kg0 = k0 + kg * KT;
+  CodeRows<DH> kc, vc;
+  auto load = [&](char* stage, int64_t row) __attribute__((always_inline)) {
+    if constexpr (k8) {
+      kc.load(gp(a.k) + row * CROW, gp(a.k_exp) + row, lane);
+      vc.load(gp(a.v) + row * CROW, gp(a.v_exp) + row, lane);
+    } else {
+      W::load(gp(a.k) + row * ROW, gp(a.v) + row * ROW, (SFN_LDS char*)stage + mine, (SFN_LDS char*)stage + STAGE + mine, lane);
+    }
+  };
+  auto put = [&](char* stage) __attribute__((always_inline)) {
+    if constexpr (k8) {
+      kc.put((SFN_LDS char*)stage + mine, lane, W::k_place);
+      vc.put((SFN_LDS char*)stage + STAGE + mine, lane, W::v_place);
+    }
+  };
   if (kg0 < k1) {
     if (lo > 0) page = page_of(kg0);
-    const int64_t at = rows_in(page, kg0);
-    W::load(gp(a.k) + at, gp(a.v) + at, (SFN_LDS char*)s_a + mine, (SFN_LDS char*)s_a + STAGE + mine, lane);
+    load(s_a, rows_in(page, kg0));
   }
 
   // this wave's rows
   const int i0 = 32 * wave, i1 = min(i0 + 31, last);  // none if i0 > last
   const int wt0 = map.token(i0), wt1 = map.token(max(i1, 0));
   const int some_hi = i0 <= last ? min(past + wt1 + 1, len) : 0;  // keys that some row of it sees
-  const int some_lo = a.window > 0 ? past + wt0 + 1 - a.window : 0;
+  const int some_lo = a.window > 0 ? past + wt0 + 1 - a.window : req.from;
   const int all_hi = min(past + wt0 + 1, len);  // and that every row sees
-  const int all_lo = a.window > 0 ? past + wt1 + 1 - a.window : 0;
+  const int all_lo = a.window > 0 ? past + wt1 + 1 - a.window : req.from;
   const bool ok = i0 + c <= last;
   const int i = ok ? i0 + c : 0, tok = map.token(i), head = hk * g + map.head(i, tok);
   w.row_hi = ok ? min(past + tok + 1, len) : 0;
-  w.row_lo = a.window > 0 ? past + tok + 1 - a.window : 0;
+  w.row_lo = a.window > 0 ? past + tok + 1 - a.window : req.from;
   w.m = kNegInf;
   w.l = 0.f;
   {
@@ -744,8 +963,9 @@ __global__ __launch_bounds__(256 * KG, 2) void attend_tile_kernel(AttendArgs a) 
   }
   auto v_row = [&](int key) {
     const int p = min(max(table[key >> lg], 0), a.n_pages - 1);
-    return gp(a.v) + ((((int64_t)p * a.h_kv + hk) << lg) + (key & pm)) * ROW;
+    return gp(a.v) + ((((int64_t)p * a.h_kv + hk) << lg) + (key & pm)) * CROW;
   };
+  if (kg0 < k1) put(s_a);
 
   // a round, a stage for each group: the keys from kr on, in cur; the next ones go into nxt
   auto round = [&](char* cur, char* nxt, int kr) __attribute__((always_inline)) {
@@ -753,7 +973,7 @@ __global__ __launch_bounds__(256 * KG, 2) void attend_tile_kernel(AttendArgs a) 
     if (kn < k1) page = page_of(kn);
     // this wave's part of the stage has arrived; after the barrier everyone's has, and the
     // other array is free
-    __builtin_amdgcn_s_waitcnt(kWaitLoads);
+    if constexpr (!k8) __builtin_amdgcn_s_waitcnt(kWaitLoads);
     __syncthreads();
     // A stage with masked keys: what the page holds past the sequence becomes 0, and so do
     // values that are not finite (0 times one of them is NaN); those count in a way of their own
@@ -771,13 +991,11 @@ __global__ __launch_bounds__(256 * KG, 2) void attend_tile_kernel(AttendArgs a) 
       }
       odd = __syncthreads_or(odd);
     }
-    if (kn < k1) {
-      const int64_t at = rows_in(page, kn);
-      W::load(gp(a.k) + at, gp(a.v) + at, (SFN_LDS char*)nxt + mine, (SFN_LDS char*)nxt + STAGE + mine, lane);
-    }
+    if (kn < k1) load(nxt, rows_in(page, kn));
     if (kt < min(some_hi, k1) && kt + KT > some_lo)
       w.step((SFN_LDS char*)cur, group, group + STAGE, kt, kt >= all_lo && kt + KT <= all_hi, odd, a.scale_log2, v_row,
              min(KT, len - kt));
+    if (k8 && kn < k1) put(nxt);
   };
   for (int kr = k0; kr < k1; kr += KG * KT) {
     round(s_a, s_b, kr);
@@ -823,7 +1041,7 @@ __global__ __launch_bounds__(256 * KG, 2) void attend_tile_kernel(AttendArgs a) 
   // every 8 of its row). 16-byte places are permuted like the stages'.
   constexpr int OC = DH / 4;  // 16-byte places of an fp32 row
   char* const out = KG == 1 ? (wave < 2 ? s_a : s_b) + (wave & 1) * 32 * DH * 4 : s_a + wave * 32 * DH * 4;
-  const bool whole = a.S == 1;
+  const bool whole = a.whole;
   const float inv = whole ? (l == 0.f ? 0.f : 1.0f / l) : 1.f;
 #pragma unroll
   for (int d = 0; d < ND; ++d)
@@ -852,6 +1070,17 @@ __global__ __launch_bounds__(256 * KG, 2) void attend_tile_kernel(AttendArgs a) 
   }
 }
 
+// The splits that wrote parts of the row of token i and head `head` of a request: those of the
+// keys that some row of its row tile saw. At most S.
+__device__ __forceinline__ int splits_used(const AttendArgs& a, const Request& req, int i, int head) {
+  const int g = a.g, rho0 = (i * g + head % g) / a.tile_rows * a.tile_rows;
+  const int rho1 = min(rho0 + a.tile_rows, min(req.n, a.max_new) * g) - 1;
+  const int hi = max(0, min(req.past + rho1 / g + 1, req.len));
+  const int lo = a.window > 0 ? max(0, req.past + rho0 / g + 1 - a.window) : req.from;
+  const int span = hi - (lo & ~(a.tile_keys - 1));
+  return span > 0 ? (span + a.chunk - 1) / a.chunk : 1;
+}
+
 // Joins the splits of one output row (a token's query head): one workgroup for a row, or one
 // wave where there are rows enough to fill the chip that way and at most 64 splits. The parts
 // lie by request and token, so that their first loads need not wait for the lengths; what
@@ -876,17 +1105,9 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a) {
 #pragma unroll
   for (int u = 0; u < U; ++u) v[u] = src[(int64_t)min(s0 + u * NS, a.S - 1) * LD];
 
-  const int t0 = min(max(gp(a.cu)[r], 0), a.T), t1 = min(max(gp(a.cu)[r + 1], t0), a.T);
-  const int n = t1 - t0;
-  if (i >= n) return;
-  const int len = min(max(gp(a.kv_len)[r], 0), a.max_len), past = len - n;
-  // the row tile that the row was in, and the keys that it saw
-  const int g = a.g, rho0 = (i * g + head % g) / a.tile_rows * a.tile_rows;
-  const int rho1 = min(rho0 + a.tile_rows, min(n, a.max_new) * g) - 1;
-  const int hi = max(0, min(past + rho1 / g + 1, len));
-  const int lo = a.window > 0 ? max(0, past + rho0 / g + 1 - a.window) : 0;
-  const int span = hi - (lo & ~(a.tile_keys - 1));
-  const int used = span > 0 ? (span + a.chunk - 1) / a.chunk : 1;  // <= S
+  const Request req(a, r);
+  if (i >= req.n) return;
+  const int t0 = req.t0, used = splits_used(a, req, i, head);
 
   const float m = tid < used ? ml[0] : kNegInf, l = tid < used ? ml[1] : 0.f;
   float M = wave_max(m);
@@ -926,6 +1147,87 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a) {
   }
 }
 
+// Joins one output row of a call over a shared prefix: the parts of the keys behind it (a, by
+// request) and of the prefix (p, by token), which count where the request's tokens come after it.
+template <int WT, int DH, bool WAVE>
+__global__ __launch_bounds__(256) void attend_join_shared_kernel(AttendArgs a, AttendArgs p) {
+  constexpr int NT = WAVE ? 64 : 256;        // threads of a row
+  constexpr int LD = DH / 4, NS = NT / LD;   // lanes of a row's values, parts side by side
+  constexpr int U = 8;                       // loads in flight
+  constexpr int NP = 2 * kMaxSplits, NK = NP / NT;
+  __shared__ float s_w[WAVE ? 4 : 1][NP];
+  __shared__ float s_red[8];
+  __shared__ f32x4_t s_o[256];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, tid = WAVE ? lane : threadIdx.x;
+  const int i = blockIdx.x, r = blockIdx.z, head = WAVE ? blockIdx.y * 4 + wave : blockIdx.y;
+  if (WAVE && head >= a.h_q) return;
+  float* const w_of = s_w[WAVE ? wave : 0];
+  const Request req(a, r);
+  if (i >= req.n) return;
+  const int shared = Request::shared_len(a);
+  const int first = min(max(gp(a.cu)[0], 0), a.T);  // the prefix's parts begin with this token
+  const int mine = splits_used(a, req, i, head);
+  const int all = mine + (req.past >= shared ? (shared + p.chunk - 1) / p.chunk : 0);
+  const int64_t at_a = (((int64_t)r * a.max_new + i) * a.h_q + head) * a.S;
+  const int64_t at_p = ((int64_t)(req.t0 + i - first) * a.h_q + head) * p.S;
+  const SFN_GLOBAL f32x2_t* ml_a = reinterpret_cast<const SFN_GLOBAL f32x2_t*>(gp(a.part_ml)) + at_a;
+  const SFN_GLOBAL f32x2_t* ml_p = reinterpret_cast<const SFN_GLOBAL f32x2_t*>(gp(p.part_ml)) + at_p;
+  const int d4 = tid % LD, s0 = tid / LD;
+  const SFN_GLOBAL f32x4_t* o_a = reinterpret_cast<const SFN_GLOBAL f32x4_t*>(gp(a.part_o) + at_a * DH) + d4;
+  const SFN_GLOBAL f32x4_t* o_p = reinterpret_cast<const SFN_GLOBAL f32x4_t*>(gp(p.part_o) + at_p * DH) + d4;
+  auto part = [&](int s) { return s < mine ? o_a[(int64_t)s * LD] : o_p[(int64_t)(s - mine) * LD]; };
+
+  float m[NK], l[NK], M = kNegInf;
+#pragma unroll
+  for (int k = 0; k < NK; ++k) {
+    const int s = tid + k * NT;
+    f32x2_t x = {kNegInf, 0.f};
+    if (s < all) x = s < mine ? ml_a[s] : ml_p[s - mine];
+    m[k] = x[0];
+    l[k] = x[1];
+    M = fmaxf(M, m[k]);
+  }
+  M = wave_max(M);
+  if constexpr (!WAVE) {
+    if (lane == 0) s_red[wave] = M;
+    __syncthreads();
+    M = fmaxf(fmaxf(s_red[0], s_red[1]), fmaxf(s_red[2], s_red[3]));
+  }
+  float L = 0.f;
+#pragma unroll
+  for (int k = 0; k < NK; ++k) {
+    const float w = m[k] == kNegInf ? 0.f : exp2_f(m[k] - M);
+    w_of[tid + k * NT] = w;
+    L += w * l[k];
+  }
+  L = wave_sum(L);
+  if constexpr (!WAVE) {
+    if (lane == 0) s_red[4 + wave] = L;
+    __syncthreads();
+    L = (s_red[4] + s_red[5]) + (s_red[6] + s_red[7]);
+  } else {
+    wave_sync();
+  }
+  f32x4_t o = {0.f, 0.f, 0.f, 0.f};
+  for (int s = s0; s < all; s += U * NS) {
+    f32x4_t v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) v[u] = part(min(s + u * NS, all - 1));
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (s + u * NS < all) o += v[u] * w_of[s + u * NS];  // also for weight 0: NaN scores show
+  }
+  f32x4_t* const o_of = s_o + (WAVE ? 64 * wave : 0);
+  o_of[tid] = o;
+  if constexpr (WAVE) wave_sync();
+  else __syncthreads();
+  if (tid < LD) {
+#pragma unroll
+    for (int s = 1; s < NS; ++s) o += o_of[s * LD + d4];
+    store_row<WT, DH>(a, req.t0 + i, head, 4 * d4, o, L);
+  }
+}
+
 // Tile kernel: up to this many workgroups get two groups of waves (one to a compute unit),
 // and few row tiles are split into at most as many. 16-token chunks of R requests, 64 / 8 heads,
 // ragged up to 4000 keys, with 256 workgroups at most, with 384 and with 512 (then one group of
@@ -941,8 +1243,8 @@ constexpr int kJoinByWave = 512;
 // items 15.5 with 8, 13.8 with 4 (three workgroups to a compute unit then), 4096 items 92 and 63.
 constexpr int kWideMost = 256;
 
-template <int WT, int DH>
-void launch_sized(const AttendArgs& a, hipStream_t stream) {
+template <int WT, int CT, int DH>
+void launch_parts(const AttendArgs& a, hipStream_t stream) {
   // heads first: the row tiles of a key head lie a multiple of h_kv apart, so that with 8 (or
   // 16, ...) key heads they share an XCD's L2
   // An odd number of splits (the one too many ends at once): workgroups go to the shader
@@ -953,24 +1255,54 @@ void launch_sized(const AttendArgs& a, hipStream_t stream) {
   if (a.tile_rows == kTileRows) {
     if constexpr (WT == WT_BF16) {
       if ((int64_t)a.R * a.S * a.row_tiles * a.h_kv > kTileFill)
-        hipLaunchKernelGGL((attend_tile_kernel<DH, 1>), grid, block, 0, stream, a);
-      else hipLaunchKernelGGL((attend_tile_kernel<DH, 2>), grid, dim3(512), 0, stream, a);
+        hipLaunchKernelGGL((attend_tile_kernel<CT, DH, 1>), grid, block, 0, stream, a);
+      else hipLaunchKernelGGL((attend_tile_kernel<CT, DH, 2>), grid, dim3(512), 0, stream, a);
     }
   } else {
     // one workgroup for all of an item's keys and a compute unit for each: more waves
     const bool wide = a.S == 1 && (int64_t)a.R * a.row_tiles * a.h_kv <= kWideMost;
     const dim3 threads(wide ? 512 : 256);
-    if (a.tile_rows == 16 && wide) hipLaunchKernelGGL((attend_split_kernel<WT, DH, 1, 8>), grid, threads, 0, stream, a);
-    else if (a.tile_rows == 16) hipLaunchKernelGGL((attend_split_kernel<WT, DH, 1, 4>), grid, threads, 0, stream, a);
-    else if (wide) hipLaunchKernelGGL((attend_split_kernel<WT, DH, 2, 8>), grid, threads, 0, stream, a);
-    else hipLaunchKernelGGL((attend_split_kernel<WT, DH, 2, 4>), grid, threads, 0, stream, a);
+    if (a.tile_rows == 16 && wide) hipLaunchKernelGGL((attend_split_kernel<WT, CT, DH, 1, 8>), grid, threads, 0, stream, a);
+    else if (a.tile_rows == 16) hipLaunchKernelGGL((attend_split_kernel<WT, CT, DH, 1, 4>), grid, threads, 0, stream, a);
+    else if (wide) hipLaunchKernelGGL((attend_split_kernel<WT, CT, DH, 2, 8>), grid, threads, 0, stream, a);
+    else hipLaunchKernelGGL((attend_split_kernel<WT, CT, DH, 2, 4>), grid, threads, 0, stream, a);
   }
+}
+
+template <int WT, int CT, int DH>
+void launch_sized(const AttendArgs& a, hipStream_t stream) {
+  launch_parts<WT, CT, DH>(a, stream);
   if (a.S > 1) {
     if (a.S <= 64 && (int64_t)a.R * a.max_new * a.h_q >= kJoinByWave)
       hipLaunchKernelGGL((attend_join_kernel<WT, DH, true>), dim3(a.max_new, (a.h_q + 3) / 4, a.R), dim3(256), 0, stream, a);
     else
       hipLaunchKernelGGL((attend_join_kernel<WT, DH, false>), dim3(a.max_new, a.h_q, a.R), dim3(256), 0, stream, a);
   }
+}
+
+template <int WT, int CT, int DH>
+void launch_shared(const AttendArgs& own, const AttendArgs& prefix, hipStream_t stream) {
+  launch_parts<WT, CT, DH>(prefix, stream);
+  launch_parts<WT, CT, DH>(own, stream);
+  if ((int64_t)own.R * own.max_new * own.h_q >= kJoinByWave)
+    hipLaunchKernelGGL((attend_join_shared_kernel<WT, DH, true>), dim3(own.max_new, (own.h_q + 3) / 4, own.R), dim3(256), 0, stream, own, prefix);
+  else
+    hipLaunchKernelGGL((attend_join_shared_kernel<WT, DH, false>), dim3(own.max_new, own.h_q, own.R), dim3(256), 0, stream, own, prefix);
+}
+
+// Calls f<WT, CT, DH>() for a cache's types and head size.
+template <class F>
+void by_type(int dh, int dtype, bool e4m3, F f) {
+  auto sized = [&](auto wt, auto ct) {
+    if (dh == 64) f(wt, ct, std::integral_constant<int, 64>());
+    else f(wt, ct, std::integral_constant<int, 128>());
+  };
+  auto typed = [&](auto wt) {
+    if (e4m3) sized(wt, std::integral_constant<int, CT_E4M3>());
+    else sized(wt, std::integral_constant<int, CT_SAME>());
+  };
+  if (dtype == SFN_BF16) typed(std::integral_constant<int, WT_BF16>());
+  else typed(std::integral_constant<int, WT_F32>());
 }
 
 }  // namespace
@@ -994,12 +1326,12 @@ void launch_sized(const AttendArgs& a, hipStream_t stream) {
 //     1016 keys 20.5 and 23.2; a prompt of 400 tokens, 32 / 8 heads, 22.2 and 14.8.
 constexpr int kPartsOfRound = 6500, kPartsOfJoin = 10000;
 constexpr int kFill = 512, kLeast = 128, kMost = 3200, kWhole = 384;
-AttendPlan attend_plan(int R, int h_q, int h_kv, int dtype, int max_new, int max_len, int window) {
+AttendPlan attend_plan(int R, int h_q, int h_kv, int dtype, bool e4m3, int max_new, int max_len, int window) {
   AttendPlan p{};
   const int64_t rows = (int64_t)max_new * (h_q / h_kv);
   const bool bf = dtype == SFN_BF16;
   p.tile_rows = rows <= 16 ? 16 : rows <= 32 || !bf ? 32 : kTileRows;
-  p.tile_keys = p.tile_rows == kTileRows ? kTileKeys : bf ? 32 : 16;
+  p.tile_keys = p.tile_rows == kTileRows ? kTileKeys : (bf ? 32 : 16) * (e4m3 ? 2 : 1);
   p.row_tiles = (int)((rows + p.tile_rows - 1) / p.tile_rows);
   const int64_t base = (int64_t)R * h_kv * p.row_tiles;
   const bool tile = p.tile_rows == kTileRows;
@@ -1029,7 +1361,7 @@ AttendPlan attend_plan(int R, int h_q, int h_kv, int dtype, int max_new, int max
 // kMost of several requests; kTileFill of the tile kernel), each with a tile's rows of parts; nor
 // can a row have more splits than its keys have steps. More new tokens may mean fewer parts (up
 // to none), so this is taken over all calls within the bounds.
-int64_t attend_most_parts(int R, int h_q, int h_kv, int dtype, int max_new, int max_len) {
+int64_t attend_most_parts(int R, int h_q, int h_kv, int dtype, bool e4m3, int max_new, int max_len) {
   const bool bf = dtype == SFN_BF16;
   const int g = h_q / h_kv;
   auto parts = [&](int64_t tokens, int64_t keys, int64_t step, int64_t rows_launched) {
@@ -1037,20 +1369,19 @@ int64_t attend_most_parts(int R, int h_q, int h_kv, int dtype, int max_new, int 
     return s > 1 ? std::min((int64_t)R * tokens * h_q * s, rows_launched) : 0;
   };
   const int64_t split = max_len <= kWhole ? 0
-                                          : parts(bf ? std::min(max_new, 32 / g) : max_new, max_len, 4 * (bf ? 32 : 16),
+                                          : parts(bf ? std::min(max_new, 32 / g) : max_new, max_len, 4 * (bf ? 32 : 16) * (e4m3 ? 2 : 1),
                                                   32 * (R > 1 ? std::max(2 * kFill, kMost) : 2 * kFill));
   const int64_t tile = bf && (int64_t)max_new * g > 32 ? parts(max_new, max_len, kTileKeys, (int64_t)kTileRows * kTileFill) : 0;
   return std::max(split, tile);
 }
 
 hipError_t launch_kv_attend(const AttendArgs& a, int dh, int dtype, hipStream_t stream) {
-  if (dtype == SFN_BF16) {
-    if (dh == 64) launch_sized<WT_BF16, 64>(a, stream);
-    else launch_sized<WT_BF16, 128>(a, stream);
-  } else {
-    if (dh == 64) launch_sized<WT_F32, 64>(a, stream);
-    else launch_sized<WT_F32, 128>(a, stream);
-  }
+  by_type(dh, dtype, a.k_exp != nullptr, [&](auto wt, auto ct, auto d) { launch_sized<wt(), ct(), d()>(a, stream); });
+  return hipGetLastError();
+}
+
+hipError_t launch_kv_attend_shared(const AttendArgs& own, const AttendArgs& prefix, int dh, int dtype, hipStream_t stream) {
+  by_type(dh, dtype, own.k_exp != nullptr, [&](auto wt, auto ct, auto d) { launch_shared<wt(), ct(), d()>(own, prefix, stream); });
   return hipGetLastError();
 }
 

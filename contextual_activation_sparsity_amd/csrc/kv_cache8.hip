@@ -1,0 +1,224 @@
+// The paged key/value cache in 8 bits: its writes (with the rotation of queries and keys) and
+// reads of whole rows.
+
+#include <algorithm>
+
+#include "cache8.h"
+#include "kernels.h"
+#include "serving_common.h"
+#include "sparse_ffn.h"
+
+namespace sfn {
+
+namespace {
+
+// ---- append --------------------------------------------------------------------------
+//
+// One workgroup per token. Queries are turned as kv_append_kernel turns them: a thread keeps
+// one 8-value unit's cosines and sines and walks the heads with them. A row of K or V (one
+// head's dh values) belongs to dh / 8 neighbouring lanes with 8 values each: the row's largest
+// magnitude is a maximum over those lanes, its power of two a shift of that maximum's bits, and
+// each value is rounded once, by the hardware's conversion to e4m3.
+// Keys are turned in 64 bits: both products of a bf16 or fp32 value and an fp32 cosine are
+// exact there, so a code is the one nearest to the rotated value but for one rounding to 53
+// bits, whatever the order of operations; in 32 bits one value in a million would fall on the
+// other side of a border between two codes. On the way to 32 bits the value is rounded to odd
+// (cut, its last bit set if anything was lost), which a second rounding does not notice.
+template <int WT>
+struct Eight;  // 8 values of a row
+template <>
+struct Eight<WT_BF16> {
+  __device__ __forceinline__ static void load(const SFN_GLOBAL char* row, int at, float* f) {
+    const uint4 v = ld16(row + at * 2);
+    const uint32_t p[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = __uint_as_float(p[i] << 16);
+      f[2 * i + 1] = __uint_as_float(p[i] & 0xffff0000u);
+    }
+  }
+  __device__ __forceinline__ static void store(SFN_GLOBAL char* row, int at, const float* f) {
+    *reinterpret_cast<SFN_GLOBAL u32x4_t*>(row + at * 2) =
+        u32x4_t{pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7])};
+  }
+};
+template <>
+struct Eight<WT_F32> {
+  __device__ __forceinline__ static void load(const SFN_GLOBAL char* row, int at, float* f) {
+#pragma unroll
+    for (int i = 0; i < 8; i += 4) {
+      const f32x4_t v = *reinterpret_cast<const SFN_GLOBAL f32x4_t*>(row + (at + i) * 4);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) f[i + j] = v[j];
+    }
+  }
+  __device__ __forceinline__ static void store(SFN_GLOBAL char* row, int at, const float* f) {
+#pragma unroll
+    for (int i = 0; i < 8; i += 4)
+      *reinterpret_cast<SFN_GLOBAL f32x4_t*>(row + (at + i) * 4) = f32x4_t{f[i], f[i + 1], f[i + 2], f[i + 3]};
+  }
+};
+
+// d in 32 bits, rounded to odd.
+__device__ __forceinline__ float to_odd(double d) {
+  uint32_t f = __float_as_uint((float)d);
+  const double back = (double)__uint_as_float(f);
+  if (back != d) f = (f - (fabs(back) > fabs(d) ? 1u : 0u)) | 1u;  // a NaN stays one
+  return __uint_as_float(f);
+}
+
+// The largest v of each N consecutive lanes (N 8 or 16), in all of them.
+template <int N>
+__device__ __forceinline__ float group_max(float v) {
+  v = fmaxf(v, dpp_mov<SFN_DPP_XOR1>(v));
+  v = fmaxf(v, dpp_mov<SFN_DPP_XOR2>(v));
+  v = fmaxf(v, dpp_mov<SFN_DPP_HALF_MIRROR>(v));
+  if constexpr (N == 16) v = fmaxf(v, dpp_mov<SFN_DPP_ROW_MIRROR>(v));
+  return v;
+}
+
+__device__ __forceinline__ bool finite(float x) { return (__float_as_uint(x) & 0x7f800000u) != 0x7f800000u; }
+
+template <int WT, int DH>
+__global__ __launch_bounds__(256) void kv8_append_kernel(Kv8AppendArgs a) {
+  constexpr int kB = WT == WT_BF16 ? 2 : 4, L = DH / 8;  // bytes of a value, lanes of a row
+  const int t = blockIdx.x, tid = threadIdx.x, nt = blockDim.x;
+  const int slot = gp(a.slot)[t];
+  const int lg = a.page_shift;
+  const bool put = slot >= 0 && (slot >> lg) < a.n_pages;  // a token without a slot writes no key or value
+  const int half = a.rot / 2;
+  const SFN_GLOBAL float* rope = nullptr;
+  if (half) rope = gp(a.rope) + (int64_t)min(max(gp(a.pos)[t], 0), a.n_pos - 1) * a.rot;
+
+  // queries
+  const SFN_GLOBAL char* q = gp(a.q) + (int64_t)t * a.q_stride;
+  SFN_GLOBAL char* qo = gp(a.q_out) + (int64_t)t * a.h_q * DH * kB;
+  const int units = half / 8;
+  if (units && a.h_q) {
+    const int u = tid % units, step = nt / units;
+    float c[8], s[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      c[i] = rope[u * 8 + i];
+      s[i] = rope[half + u * 8 + i];
+    }
+    for (int h = tid / units; h < a.h_q && tid < units * step; h += step) {
+      float x[8], y[8], xr[8], yr[8];
+      Eight<WT>::load(q + h * DH * kB, u * 8, x);
+      Eight<WT>::load(q + h * DH * kB, half + u * 8, y);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        xr[i] = x[i] * c[i] - y[i] * s[i];
+        yr[i] = y[i] * c[i] + x[i] * s[i];
+      }
+      Eight<WT>::store(qo + h * DH * kB, u * 8, xr);
+      Eight<WT>::store(qo + h * DH * kB, half + u * 8, yr);
+    }
+  }
+  const int rest = (DH - a.rot) / 8;  // eights of a head that are not turned
+  for (int i = tid; i < a.h_q * rest; i += nt) {
+    const int h = i / rest, at = a.rot + (i % rest) * 8;
+    float x[8];
+    Eight<WT>::load(q + h * DH * kB, at, x);
+    Eight<WT>::store(qo + h * DH * kB, at, x);
+  }
+  if (!put) return;
+
+  // keys, then values; whole waves take part in the maxima
+  const int64_t cell = (((int64_t)(slot >> lg) * a.h_kv) << lg) + (slot & ((1 << lg) - 1));  // head 0's row in the cache
+  const int rows = 2 * a.h_kv, j8 = (tid % L) * 8;
+  for (int r0 = 0; r0 < rows; r0 += nt / L) {
+    const int r = r0 + tid / L;
+    const bool mine = r < rows, key = r < a.h_kv;
+    const int h = key ? r : r - a.h_kv;
+    float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (mine) {
+      const SFN_GLOBAL char* row = (key ? gp(a.k) + (int64_t)t * a.k_stride : gp(a.v) + (int64_t)t * a.v_stride) + h * DH * kB;
+      Eight<WT>::load(row, j8, x);
+      if (key && j8 < a.rot) {
+        const bool low = j8 < half;
+        const int at = low ? j8 : j8 - half;
+        float y[8];
+        Eight<WT>::load(row, low ? j8 + half : at, y);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const double sn = low ? -(double)rope[half + at + i] : (double)rope[half + at + i];
+          x[i] = to_odd((double)x[i] * (double)rope[at + i] + (double)y[i] * sn);
+        }
+      }
+    }
+    float top = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = fmaxf(top, finite(x[i]) ? fabsf(x[i]) : 0.f);
+    const int b = exp_of_row(group_max<L>(top));
+    const float scale = __uint_as_float((uint32_t)(254 - b) << 23);  // 2^(127 - b)
+    float y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)  // e4m3 has no infinity: it becomes NaN, as NaN does
+      y[i] = finite(x[i]) ? fminf(fmaxf(x[i] * scale, -448.f), 448.f) : __uint_as_float(0x7fc00000u);
+    if (mine) {
+      const int64_t to = cell + ((int64_t)h << lg);
+      *reinterpret_cast<SFN_GLOBAL uint64_t*>((key ? gp(a.k_cache) : gp(a.v_cache)) + to * DH + j8) =
+          (uint64_t)pack_e4m3(y[0], y[1], y[2], y[3]) | (uint64_t)pack_e4m3(y[4], y[5], y[6], y[7]) << 32;
+      if (j8 == 0) (key ? gp(a.k_exp) : gp(a.v_exp))[to] = (uint8_t)b;
+    }
+  }
+}
+
+// ---- read ----------------------------------------------------------------------------
+//
+// Rows of K and V by slots, as the values they stand for: exact in bf16 and fp32 (four bits of
+// significand and a power of two). A lane turns 8 codes; a token is one workgroup's.
+template <int WT, int DH>
+__global__ __launch_bounds__(256) void kv8_read_kernel(Kv8ReadArgs a) {
+  constexpr int kB = WT == WT_BF16 ? 2 : 4, L = DH / 8;
+  const int t = blockIdx.x, lg = a.page_shift;
+  const int slot = gp(a.slot)[t];
+  const bool held = slot >= 0 && (slot >> lg) < a.n_pages;
+  const int64_t cell = held ? (((int64_t)(slot >> lg) * a.h_kv) << lg) + (slot & ((1 << lg) - 1)) : 0;
+  for (int i = threadIdx.x; i < 2 * a.h_kv * L; i += blockDim.x) {
+    const int r = i / L, j8 = (i % L) * 8;
+    const bool key = r < a.h_kv;
+    const int h = key ? r : r - a.h_kv;
+    const int64_t from = cell + ((int64_t)h << lg);
+    float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (held) {
+      const uint64_t w = *reinterpret_cast<const SFN_GLOBAL uint64_t*>((key ? gp(a.k_cache) : gp(a.v_cache)) + from * DH + j8);
+      const float scale = scale_of((key ? gp(a.k_exp) : gp(a.v_exp))[from]);
+      values_of((uint32_t)w, scale, x);
+      values_of((uint32_t)(w >> 32), scale, x + 4);
+    }
+    Eight<WT>::store((key ? gp(a.k_out) + (int64_t)t * a.k_stride : gp(a.v_out) + (int64_t)t * a.v_stride) + h * DH * kB, j8, x);
+  }
+}
+
+int threads_for(int items) { return items <= 64 ? 64 : items <= 128 ? 128 : 256; }
+
+template <int WT>
+void launch_append(const Kv8AppendArgs& a, int dh, int threads, hipStream_t stream) {
+  if (dh == 64) hipLaunchKernelGGL((kv8_append_kernel<WT, 64>), dim3(a.T), dim3(threads), 0, stream, a);
+  else hipLaunchKernelGGL((kv8_append_kernel<WT, 128>), dim3(a.T), dim3(threads), 0, stream, a);
+}
+template <int WT>
+void launch_read(const Kv8ReadArgs& a, int dh, int threads, hipStream_t stream) {
+  if (dh == 64) hipLaunchKernelGGL((kv8_read_kernel<WT, 64>), dim3(a.T), dim3(threads), 0, stream, a);
+  else hipLaunchKernelGGL((kv8_read_kernel<WT, 128>), dim3(a.T), dim3(threads), 0, stream, a);
+}
+
+}  // namespace
+
+hipError_t launch_kv8_append(const Kv8AppendArgs& a, int dh, int dtype, hipStream_t stream) {
+  const int threads = threads_for(std::max(a.h_q * std::max(a.rot / 2, dh - a.rot) / 8, 2 * a.h_kv * dh / 8));
+  if (dtype == SFN_BF16) launch_append<WT_BF16>(a, dh, threads, stream);
+  else launch_append<WT_F32>(a, dh, threads, stream);
+  return hipGetLastError();
+}
+
+hipError_t launch_kv8_read(const Kv8ReadArgs& a, int dh, int dtype, hipStream_t stream) {
+  const int threads = threads_for(2 * a.h_kv * dh / 8);
+  if (dtype == SFN_BF16) launch_read<WT_BF16>(a, dh, threads, stream);
+  else launch_read<WT_F32>(a, dh, threads, stream);
+  return hipGetLastError();
+}
+
+}  // namespace sfn

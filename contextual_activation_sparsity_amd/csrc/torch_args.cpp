@@ -21,6 +21,19 @@ decltype(&kv_cache_plan) f_plan;
 decltype(&kv_cache_append) f_append;
 decltype(&kv_cache_attend) f_attend;
 decltype(&residual_norm) f_norm;
+decltype(&kv8_cache_append) f_append8;
+decltype(&kv8_cache_read) f_read8;
+decltype(&kv8_cache_attend) f_attend8;
+decltype(&kv_cache_attend_shared) f_attend_shared;
+decltype(&kv8_cache_attend_shared) f_attend_shared8;
+
+// The device that the call in hand is for, where its tensors have to be on it: -1 if that is
+// not asked.
+thread_local int64_t t_device = -1;
+struct OnDevice {
+  explicit OnDevice(int64_t d) { t_device = d; }
+  ~OnDevice() { t_device = -1; }
+};
 
 constexpr at::ScalarType kAny = at::ScalarType::Undefined;
 
@@ -35,7 +48,11 @@ const at::Tensor* tensor(PyObject* o, const char* name) {
     return nullptr;
   }
   const at::Tensor& t = THPVariable_Unpack(o);
-  if (t.is_cuda()) return &t;
+  if (t.is_cuda()) {
+    if (t_device < 0 || !t.device().has_index() || t.device().index() == t_device) return &t;
+    fail(PyExc_ValueError, std::string(name) + " is on " + t.device().str() + ", the call is for cuda:" + std::to_string(t_device));
+    return nullptr;
+  }
   fail(PyExc_ValueError, std::string(name) + " must be a GPU tensor (got " + t.device().str() + ")");
   return nullptr;
 }
@@ -109,6 +126,17 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (PyErr_Occurred()) return nullptr;
   Py_RETURN_NONE;
 }
+// (append8, read8, attend8, attend_shared, attend_shared8)
+PyObject* bind_more(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!count(n, 5)) return nullptr;
+  f_append8 = reinterpret_cast<decltype(f_append8)>(pointer(a[0]));
+  f_read8 = reinterpret_cast<decltype(f_read8)>(pointer(a[1]));
+  f_attend8 = reinterpret_cast<decltype(f_attend8)>(pointer(a[2]));
+  f_attend_shared = reinterpret_cast<decltype(f_attend_shared)>(pointer(a[3]));
+  f_attend_shared8 = reinterpret_cast<decltype(f_attend_shared8)>(pointer(a[4]));
+  if (PyErr_Occurred()) return nullptr;
+  Py_RETURN_NONE;
+}
 
 // (sfn_kv address, held_len, ctx_len, new_len, table, free_pages, n_free, n_free_out, cu,
 // kv_len, pos, slot, status, stream)
@@ -142,22 +170,20 @@ PyObject* plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// (sfn_kv address, k, v, slot, q, q_out, pos, rope, stream)
-PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (!count(n, 9)) return nullptr;
-  const sfn_kv* kv = static_cast<const sfn_kv*>(pointer(a[0]));
-  if (!kv) return status(SFN_EINVAL);
+// a: k, v, slot, q, q_out, pos, rope, stream; call(...) takes kv_cache_append's arguments after kv
+template <class Call>
+PyObject* append_with(const sfn_kv* kv, PyObject* const* a, Call call) {
   const at::ScalarType dt = cache_type(kv);
   void *k, *v, *q = nullptr, *slot, *q_out, *pos, *rope;
   int64_t T = -1, ks, vs, qs = 0, h_kv = kv->h_kv, h_q = -1, n_pos = 0, rot = 0;
-  if (!token_rows(a[1], "k", dt, &T, &h_kv, kv->dh, &k, &ks) || !token_rows(a[2], "v", dt, &T, &h_kv, kv->dh, &v, &vs)) return nullptr;
-  if (a[4] == Py_None) h_q = 0;
-  else if (!token_rows(a[4], "q", dt, &T, &h_q, kv->dh, &q, &qs)) return nullptr;
-  if (!ints(a[3], "slot", T, &slot) || !address(a[5], "q_out", dt, T * h_q * kv->dh, &q_out) || !ints(a[6], "pos", T, &pos) ||
-      !address(a[7], "rope", at::kFloat, 0, &rope))
+  if (!token_rows(a[0], "k", dt, &T, &h_kv, kv->dh, &k, &ks) || !token_rows(a[1], "v", dt, &T, &h_kv, kv->dh, &v, &vs)) return nullptr;
+  if (a[3] == Py_None) h_q = 0;
+  else if (!token_rows(a[3], "q", dt, &T, &h_q, kv->dh, &q, &qs)) return nullptr;
+  if (!ints(a[2], "slot", T, &slot) || !address(a[4], "q_out", dt, T * h_q * kv->dh, &q_out) || !ints(a[5], "pos", T, &pos) ||
+      !address(a[6], "rope", at::kFloat, 0, &rope))
     return nullptr;
   if (rope) {
-    const at::Tensor& t = THPVariable_Unpack(a[7]);
+    const at::Tensor& t = THPVariable_Unpack(a[6]);
     if (t.dim() != 2) {
       fail(PyExc_ValueError, "rope must be [n_pos, rot]");
       return nullptr;
@@ -166,11 +192,82 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     rot = t.size(1);
   }
   if (!fits(T, "T") || !fits(h_q, "h_q") || !fits(n_pos, "n_pos") || !fits(rot, "rot")) return nullptr;
-  void* stream = pointer(a[8]);
+  void* stream = pointer(a[7]);
   if (PyErr_Occurred()) return nullptr;
   return status_of([&] {
-    return f_append(kv, (int32_t)T, (int32_t)h_q, q, qs, k, ks, v, vs, static_cast<int32_t*>(pos), static_cast<int32_t*>(slot),
+    return call((int32_t)T, (int32_t)h_q, q, qs, k, ks, v, vs, static_cast<int32_t*>(pos), static_cast<int32_t*>(slot),
                     static_cast<float*>(rope), (int32_t)n_pos, (int32_t)rot, q_out, stream);
+  });
+}
+
+// (sfn_kv address, k, v, slot, q, q_out, pos, rope, stream)
+PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!count(n, 9)) return nullptr;
+  const sfn_kv* kv = static_cast<const sfn_kv*>(pointer(a[0]));
+  if (!kv) return status(SFN_EINVAL);
+  return append_with(kv, a + 1, [&](auto... x) { return f_append(kv, x...); });
+}
+
+// (sfn_kv8 address, k, v, slot, q, q_out, pos, rope, stream, device)
+PyObject* append8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!count(n, 10)) return nullptr;
+  const sfn_kv8* kv = static_cast<const sfn_kv8*>(pointer(a[0]));
+  if (!kv) return status(SFN_EINVAL);
+  const OnDevice on(PyLong_AsLongLong(a[9]));
+  if (PyErr_Occurred()) return nullptr;
+  return append_with(&kv->kv, a + 1, [&](auto... x) { return f_append8(kv, x...); });
+}
+
+// (sfn_kv8 address, slot, k_out, v_out, stream, device)
+PyObject* read8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!count(n, 6)) return nullptr;
+  const sfn_kv8* kv = static_cast<const sfn_kv8*>(pointer(a[0]));
+  if (!kv) return status(SFN_EINVAL);
+  const OnDevice on(PyLong_AsLongLong(a[5]));
+  if (PyErr_Occurred()) return nullptr;
+  const at::ScalarType dt = cache_type(&kv->kv);
+  void *k, *v, *slot;
+  int64_t T = -1, h_kv = kv->kv.h_kv, ks, vs;
+  if (!token_rows(a[2], "k_out", dt, &T, &h_kv, kv->kv.dh, &k, &ks) || !token_rows(a[3], "v_out", dt, &T, &h_kv, kv->kv.dh, &v, &vs) ||
+      !ints(a[1], "slot", T, &slot) || !fits(T, "T"))
+    return nullptr;
+  void* stream = pointer(a[4]);
+  if (PyErr_Occurred()) return nullptr;
+  return status_of([&] { return f_read8(kv, (int32_t)T, static_cast<int32_t*>(slot), k, ks, v, vs, stream); });
+}
+
+// a: q, table, cu, kv_len, out, ws, max_new, max_len, scale, window, stream
+template <class Call>
+PyObject* attend_with(const sfn_kv* kv, PyObject* const* a, Call call) {
+  const at::ScalarType dt = cache_type(kv);
+  void *q, *table, *cu, *kv_len, *out, *ws;
+  int64_t T = -1, h_q = -1, qs, R = 0, cols = 0;
+  if (!token_rows(a[0], "q", dt, &T, &h_q, kv->dh, &q, &qs) || !ints(a[1], "table", 0, &table)) return nullptr;
+  if (table) {
+    const at::Tensor& t = THPVariable_Unpack(a[1]);
+    if (t.dim() != 2) {
+      fail(PyExc_ValueError, "table must be [R, max_pages]");
+      return nullptr;
+    }
+    R = t.size(0);
+    cols = t.size(1);
+  }
+  if (!ints(a[2], "cu", R + 1, &cu) || !ints(a[3], "kv_len", R, &kv_len) || !address(a[4], "out", dt, T * h_q * kv->dh, &out) ||
+      !address(a[5], "ws", kAny, 0, &ws))
+    return nullptr;
+  const size_t ws_bytes = ws ? THPVariable_Unpack(a[5]).nbytes() : 0;
+  const long long max_new = PyLong_AsLongLong(a[6]), max_len = PyLong_AsLongLong(a[7]), window = PyLong_AsLongLong(a[9]);
+  const double scale = PyFloat_AsDouble(a[8]);
+  void* stream = pointer(a[10]);
+  if (PyErr_Occurred()) return nullptr;
+  if (!fits(T, "T") || !fits(h_q, "h_q") || !fits(R, "R") || !fits(cols, "max_pages") || !fits(max_new, "max_new") ||
+      !fits(max_len, "max_len") || !fits(window, "window"))
+    return nullptr;
+  auto clamp = [](long long v) { return (int32_t)(v < -1 ? -1 : v); };
+  return status_of([&] {
+    return call((int32_t)R, (int32_t)T, (int32_t)h_q, q, qs, static_cast<int32_t*>(table), (int32_t)cols,
+                    static_cast<int32_t*>(cu), static_cast<int32_t*>(kv_len), clamp(max_new), clamp(max_len), (float)scale,
+                    clamp(window), out, ws, ws_bytes, stream);
   });
 }
 
@@ -179,12 +276,32 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!count(n, 12)) return nullptr;
   const sfn_kv* kv = static_cast<const sfn_kv*>(pointer(a[0]));
   if (!kv) return status(SFN_EINVAL);
+  return attend_with(kv, a + 1, [&](auto... x) { return f_attend(kv, x...); });
+}
+
+// (sfn_kv8 address, q, table, cu, kv_len, out, ws, max_new, max_len, scale, window, stream, device)
+PyObject* attend8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!count(n, 13)) return nullptr;
+  const sfn_kv8* kv = static_cast<const sfn_kv8*>(pointer(a[0]));
+  if (!kv) return status(SFN_EINVAL);
+  const OnDevice on(PyLong_AsLongLong(a[12]));
+  if (PyErr_Occurred()) return nullptr;
+  return attend_with(&kv->kv, a + 1, [&](auto... x) { return f_attend8(kv, x...); });
+}
+
+// a: q, prefix, shared_len, table, cu, kv_len, out, ws, max_new, max_shared, max_own, scale, stream, device
+template <class Call>
+PyObject* attend_shared_with(const sfn_kv* kv, PyObject* const* a, Call call) {
+  const OnDevice on(PyLong_AsLongLong(a[13]));
+  if (PyErr_Occurred()) return nullptr;
   const at::ScalarType dt = cache_type(kv);
-  void *q, *table, *cu, *kv_len, *out, *ws;
-  int64_t T = -1, h_q = -1, qs, R = 0, cols = 0;
-  if (!token_rows(a[1], "q", dt, &T, &h_q, kv->dh, &q, &qs) || !ints(a[2], "table", 0, &table)) return nullptr;
-  if (table) {
-    const at::Tensor& t = THPVariable_Unpack(a[2]);
+  void *q, *prefix, *shared, *table, *cu, *kv_len, *out, *ws;
+  int64_t T = -1, h_q = -1, qs, R = 0, cols = 0, pages = 0;
+  if (!token_rows(a[0], "q", dt, &T, &h_q, kv->dh, &q, &qs) || !ints(a[1], "prefix", 0, &prefix) || !ints(a[3], "table", 0, &table))
+    return nullptr;
+  if (a[1] != Py_None) pages = THPVariable_Unpack(a[1]).numel();
+  if (a[3] != Py_None) {
+    const at::Tensor& t = THPVariable_Unpack(a[3]);
     if (t.dim() != 2) {
       fail(PyExc_ValueError, "table must be [R, max_pages]");
       return nullptr;
@@ -192,23 +309,39 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
     R = t.size(0);
     cols = t.size(1);
   }
-  if (!ints(a[3], "cu", R + 1, &cu) || !ints(a[4], "kv_len", R, &kv_len) || !address(a[5], "out", dt, T * h_q * kv->dh, &out) ||
-      !address(a[6], "ws", kAny, 0, &ws))
+  if (!ints(a[2], "shared_len", 1, &shared) || !ints(a[4], "cu", R + 1, &cu) || !ints(a[5], "kv_len", R, &kv_len) ||
+      !address(a[6], "out", dt, T * h_q * kv->dh, &out) || !address(a[7], "ws", kAny, 0, &ws))
     return nullptr;
-  const size_t ws_bytes = ws ? THPVariable_Unpack(a[6]).nbytes() : 0;
-  const long long max_new = PyLong_AsLongLong(a[7]), max_len = PyLong_AsLongLong(a[8]), window = PyLong_AsLongLong(a[10]);
-  const double scale = PyFloat_AsDouble(a[9]);
-  void* stream = pointer(a[11]);
+  const size_t ws_bytes = ws ? THPVariable_Unpack(a[7]).nbytes() : 0;
+  const long long max_new = PyLong_AsLongLong(a[8]), max_shared = PyLong_AsLongLong(a[9]), max_own = PyLong_AsLongLong(a[10]);
+  const double scale = PyFloat_AsDouble(a[11]);
+  void* stream = pointer(a[12]);
   if (PyErr_Occurred()) return nullptr;
-  if (!fits(T, "T") || !fits(h_q, "h_q") || !fits(R, "R") || !fits(cols, "max_pages") || !fits(max_new, "max_new") ||
-      !fits(max_len, "max_len") || !fits(window, "window"))
+  if (!fits(T, "T") || !fits(h_q, "h_q") || !fits(R, "R") || !fits(cols, "max_pages") || !fits(pages, "the number of prefix pages") ||
+      !fits(max_new, "max_new") || !fits(max_shared, "max_shared") || !fits(max_own, "max_own"))
     return nullptr;
   auto clamp = [](long long v) { return (int32_t)(v < -1 ? -1 : v); };
+  auto i = [](void* p) { return static_cast<const int32_t*>(p); };
   return status_of([&] {
-    return f_attend(kv, (int32_t)R, (int32_t)T, (int32_t)h_q, q, qs, static_cast<int32_t*>(table), (int32_t)cols,
-                    static_cast<int32_t*>(cu), static_cast<int32_t*>(kv_len), clamp(max_new), clamp(max_len), (float)scale,
-                    clamp(window), out, ws, ws_bytes, stream);
+    return call((int32_t)R, (int32_t)T, (int32_t)h_q, q, qs, i(prefix), (int32_t)pages, i(shared), i(table), (int32_t)cols, i(cu), i(kv_len),
+                clamp(max_new), clamp(max_shared), clamp(max_own), (float)scale, out, ws, ws_bytes, stream);
   });
+}
+
+// (sfn_kv address, q, prefix, shared_len, table, cu, kv_len, out, ws, max_new, max_shared, max_own, scale, stream, device)
+PyObject* attend_shared(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!count(n, 15)) return nullptr;
+  const sfn_kv* kv = static_cast<const sfn_kv*>(pointer(a[0]));
+  if (!kv) return status(SFN_EINVAL);
+  return attend_shared_with(kv, a + 1, [&](auto... x) { return f_attend_shared(kv, x...); });
+}
+
+// The same with an sfn_kv8 address.
+PyObject* attend_shared8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!count(n, 15)) return nullptr;
+  const sfn_kv8* kv = static_cast<const sfn_kv8*>(pointer(a[0]));
+  if (!kv) return status(SFN_EINVAL);
+  return attend_shared_with(&kv->kv, a + 1, [&](auto... x) { return f_attend_shared8(kv, x...); });
 }
 
 // (sfn_norm address, h, y, h_out, x_out, gate, stream)
@@ -268,8 +401,10 @@ template <Fast F>
 PyMethodDef method(const char* name) {
   return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&raising<F>)), METH_FASTCALL, nullptr};
 }
-PyMethodDef methods[] = {method<bind>("bind"),     method<plan>("plan"), method<append>("append"),
-                         method<attend>("attend"), method<norm>("norm"), {nullptr, nullptr, 0, nullptr}};
+PyMethodDef methods[] = {method<bind>("bind"),       method<plan>("plan"),     method<append>("append"),
+                         method<attend>("attend"),   method<norm>("norm"),     method<append8>("append8"),
+                         method<read8>("read8"),     method<attend8>("attend8"), method<attend_shared>("attend_shared"),
+                         method<attend_shared8>("attend_shared8"), method<bind_more>("bind_more"), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_torch_args", nullptr, -1, methods};
 
 }  // namespace

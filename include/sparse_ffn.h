@@ -393,6 +393,91 @@ int kv_cache_attend(const sfn_kv* kv, int32_t R, int32_t T, int32_t h_q, const v
                     int32_t max_new, int32_t max_len, float scale, int32_t window, void* out, void* ws,
                     size_t ws_bytes, void* stream);
 
+/*
+ * Attention of requests whose first tokens are the same (a system prompt, a document): the same
+ * results as kv_cache_attend's without a window, but the keys and values of the first
+ * *shared_len tokens are read once for all requests of the call, from the pages in `prefix`, and
+ * those after them from each request's own row of the table. The rows are those of
+ * kv_cache_attend: they, and kv_len, count the shared tokens too. Of row entries only those of
+ * the pages from token *shared_len on are read, for a request whose new tokens all come after
+ * the shared ones (kv_len - n >= *shared_len); a request of which that is not so reads all its
+ * keys from its own row. Whole shared pages may simply stand in every row (a plan whose ctx_len
+ * stays at or above the shared tokens gives none of them back); *shared_len need not be a
+ * multiple of the page.
+ *   prefix   [prefix_pages]: the pages of the shared tokens, in order (clamped like the table's)
+ *   shared_len  1 int32, read
+ *   max_new  as in kv_cache_attend
+ *   max_shared, max_own  bounds, together up to 2^30, on *shared_len and on the keys that a
+ *            request reads from its own row. As there, lengths past them stay in bounds:
+ *            *shared_len counts as max_shared (or the tokens of prefix_pages) at most, a kv_len as
+ *            *shared_len + max_own at most, or as max_own where the request reads its own row alone
+ * Requests with other prefixes are calls of their own (with rows of table, cu and kv_len, as
+ * above). Workspace: as kv_cache_attend's, enough for every call with smaller arguments.
+ * T = 0 does nothing.
+ */
+size_t kv_cache_attend_shared_workspace_size(const sfn_kv* kv, int32_t R, int32_t T, int32_t h_q, int32_t max_new,
+                                             int32_t max_shared, int32_t max_own);
+int kv_cache_attend_shared(const sfn_kv* kv, int32_t R, int32_t T, int32_t h_q, const void* q, int64_t q_stride,
+                           const int32_t* prefix, int32_t prefix_pages, const int32_t* shared_len,
+                           const int32_t* table, int32_t max_pages, const int32_t* cu, const int32_t* kv_len,
+                           int32_t max_new, int32_t max_shared, int32_t max_own, float scale, void* out, void* ws,
+                           size_t ws_bytes, void* stream);
+
+/*
+ * ---- The cache in 8 bits ----------------------------------------------------------------
+ *
+ * Half the bytes of bf16, a quarter of fp32. A row (one head's dh keys or values of a token) is
+ * held as e4m3 codes (a sign, 4 bits of exponent, 3 of significand; largest value 448, no
+ * infinity, NaN 0x7f and 0xff) and one byte b: value i is code_i * 2^(b - 127). Of each row b is the
+ * least with which its largest finite magnitude is at most 448 * 2^(b - 127), at least 10 and at
+ * most 246, so that every code's value is finite and exact in bf16 and fp32, and a value is off
+ * by at most 2^-4 of itself, or by 2^(b - 137) where it is below 2^(b - 133). Magnitudes above
+ * 448 * 2^119 (near the end of bf16's range) become that; infinities become NaN. Readers take a
+ * byte outside [10, 246] as the nearest of those.
+ * kv.dtype is the type of q, k, v and of the results; kv.k and kv.v hold the codes. The plan is
+ * kv_cache_plan, which reads the shape alone (&kv8.kv).
+ */
+typedef struct sfn_kv8 {
+  sfn_kv kv;      /* k and v: [n_pages, h_kv, page, dh] e4m3 codes */
+  uint8_t* k_exp; /* [n_pages, h_kv, page]: the rows' bytes; 16-byte aligned */
+  uint8_t* v_exp;
+} sfn_kv8;
+
+/*
+ * kv_cache_append into that cache. Keys are rotated in 64 bits and rounded once, to the nearest
+ * code (ties to the even one); values are rounded once; q as there.
+ */
+int kv8_cache_append(const sfn_kv8* kv, int32_t T, int32_t h_q, const void* q, int64_t q_stride, const void* k,
+                     int64_t k_stride, const void* v, int64_t v_stride, const int32_t* pos, const int32_t* slot,
+                     const float* rope, int32_t n_pos, int32_t rot, void* q_out, void* stream);
+
+/*
+ * Reads tokens' keys and values back, by slots (as kv_cache_append takes them; any order, a slot
+ * as often as wanted): to keep a request's tokens elsewhere, or to append them to another cache.
+ *   slot     [T]; a slot outside the cache gives zeros
+ *   k_out, v_out  token t's heads at k_out + t * k_stride (elements), each head's dh values
+ *            contiguous, in kv.dtype, exact; addresses and strides 16-byte aligned
+ * T = 0 does nothing.
+ */
+int kv8_cache_read(const sfn_kv8* kv, int32_t T, const int32_t* slot, void* k_out, int64_t k_stride, void* v_out,
+                   int64_t v_stride, void* stream);
+
+/* kv_cache_attend and kv_cache_attend_shared over that cache: of the values that the codes
+ * stand for, with the same arithmetic. A NaN code reaches only the tokens that see its key. */
+size_t kv8_cache_attend_workspace_size(const sfn_kv8* kv, int32_t R, int32_t T, int32_t h_q, int32_t max_new,
+                                       int32_t max_len);
+int kv8_cache_attend(const sfn_kv8* kv, int32_t R, int32_t T, int32_t h_q, const void* q, int64_t q_stride,
+                     const int32_t* table, int32_t max_pages, const int32_t* cu, const int32_t* kv_len,
+                     int32_t max_new, int32_t max_len, float scale, int32_t window, void* out, void* ws,
+                     size_t ws_bytes, void* stream);
+size_t kv8_cache_attend_shared_workspace_size(const sfn_kv8* kv, int32_t R, int32_t T, int32_t h_q, int32_t max_new,
+                                              int32_t max_shared, int32_t max_own);
+int kv8_cache_attend_shared(const sfn_kv8* kv, int32_t R, int32_t T, int32_t h_q, const void* q, int64_t q_stride,
+                            const int32_t* prefix, int32_t prefix_pages, const int32_t* shared_len,
+                            const int32_t* table, int32_t max_pages, const int32_t* cu, const int32_t* kv_len,
+                            int32_t max_new, int32_t max_shared, int32_t max_own, float scale, void* out, void* ws,
+                            size_t ws_bytes, void* stream);
+
 /* The norms on either side of the residual stream's update. All pointers device. */
 typedef struct sfn_norm {
   int32_t d;          /* hidden size, a multiple of 8, at most SFN_MAX_D */

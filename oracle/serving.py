@@ -99,3 +99,43 @@ def residual_norm(h, y, w_pre=None, w_post=None, gate=None, scale=1.0, eps=1e-5)
             u = u * np.asarray(gate, dtype=np.float64)
         h = h + scale * u
     return h, None if w_pre is None else rms_norm(h, w_pre, eps)
+
+
+# ---- the cache in 8 bits --------------------------------------------------------------
+
+EXP_LEAST, EXP_MOST = 10, 246  # a row's byte b stands for 2^(b - 127)
+
+
+def e4m3_values():
+    """What the 256 codes stand for: a sign, 4 bits of exponent (bias 7; 0 for subnormal), 3 of
+    significand; 0x7f and 0xff are NaN and there is no infinity."""
+    c = np.arange(128)
+    v = np.where(c >= 8, (8 + c % 8) * 2.0 ** (c // 8 - 10), (c % 8) * 2.0 ** -9)
+    v[127] = np.nan
+    return np.concatenate([v, -v])
+
+
+def stand_for(codes, b):
+    """Values of codes [..., dh] and their rows' bytes b [...]."""
+    b = np.clip(np.asarray(b, dtype=np.int64), EXP_LEAST, EXP_MOST)
+    return e4m3_values()[np.asarray(codes)] * (2.0 ** (b - 127.0))[..., None]
+
+
+def quantise(x):
+    """(codes, bytes) of rows x [..., dh]: per row the least power of two with which 448 times it
+    is not below the largest finite magnitude, and of each value the nearest code, ties to the
+    even one; magnitudes past the largest code become it, infinities and NaN become NaN."""
+    x = np.asarray(x, dtype=np.float64)
+    ok = np.isfinite(x)
+    top = np.where(ok, np.abs(x), 0.0).max(axis=-1)
+    b = np.full(top.shape, EXP_LEAST, dtype=np.int64)
+    for e in range(EXP_LEAST, EXP_MOST):
+        b = np.where(top > 448.0 * 2.0 ** (e - 127), e + 1, b)
+    vals = e4m3_values()[:127]
+    y = np.minimum(np.abs(np.where(ok, x, 0.0)) * (2.0 ** (127.0 - b))[..., None], 448.0)
+    up = np.minimum(np.searchsorted(vals, y), 126)
+    down = np.maximum(up - 1, 0)
+    mid = (vals[up] + vals[down]) / 2
+    code = np.where((y > mid) | ((y == mid) & (up % 2 == 0)), up, down)
+    code = np.where(y == vals[up], up, code)
+    return np.where(ok, code + 128 * np.signbit(np.where(ok, x, 0.0)), 127).astype(np.uint8), b.astype(np.uint8)
