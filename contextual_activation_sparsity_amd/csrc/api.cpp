@@ -583,9 +583,9 @@ int kv8_cache_read(const sfn_kv8* kv, int32_t T, const int32_t* slot, void* k_ou
 
 namespace {
 
-size_t attend_size(const sfn_kv* kv, bool e4m3, int32_t R, int32_t T, int32_t h_q, int32_t max_new, int32_t max_len) {
+size_t attend_size(const sfn_kv* kv, int32_t R, int32_t T, int32_t h_q, int32_t max_new, int32_t max_len) {
   if (check_attend(kv, R, T, h_q, max_new, max_len) != SFN_OK) return 0;
-  return attend_bytes(kv, sfn::attend_most_parts(R, h_q, kv->h_kv, kv->dtype, e4m3, max_new, max_len));
+  return attend_bytes(kv, sfn::attend_most_parts(R, h_q, kv->h_kv, kv->dtype, max_new, max_len));
 }
 
 // What every attention launch has in common.
@@ -636,7 +636,7 @@ int attend(const sfn_kv* kv, const uint8_t* k_exp, const uint8_t* v_exp, int32_t
   if ((st = check_rows(q, q_stride, h_q, kv)) != SFN_OK) return st;
   if (!aligned16(out) || !aligned4_or_null(table) || !aligned4_or_null(cu) || !aligned4_or_null(kv_len)) return SFN_EALIGN;
   if (window >= max_len) window = 0;  // every key is within it
-  const sfn::AttendPlan p = sfn::attend_plan(R, h_q, kv->h_kv, kv->dtype, k_exp != nullptr, max_new, max_len, window);
+  const sfn::AttendPlan p = sfn::attend_plan(R, h_q, kv->h_kv, kv->dtype, max_new, max_len, window);
   if ((int64_t)R * p.S * p.row_tiles * kv->h_kv > INT32_MAX) return SFN_ESHAPE;
   if ((st = check_ws(ws, ws_bytes, attend_bytes(kv, p.parts))) != SFN_OK) return st;
   sfn::AttendArgs a = attend_args(kv, k_exp, v_exp, T, h_q, q, q_stride, cu, kv_len, scale, out);
@@ -668,11 +668,11 @@ size_t shared_bytes(const sfn_kv* kv, int64_t own, int64_t prefix) {
   return attend_bytes(kv, own) + attend_bytes(kv, prefix) - sfn::kWsHeader;
 }
 
-size_t shared_size(const sfn_kv* kv, bool e4m3, int32_t R, int32_t T, int32_t h_q, int32_t max_new, int32_t max_shared, int32_t max_own) {
+size_t shared_size(const sfn_kv* kv, int32_t R, int32_t T, int32_t h_q, int32_t max_new, int32_t max_shared, int32_t max_own) {
   if (check_shared(kv, R, T, h_q, max_new, max_shared, max_own) != SFN_OK) return 0;
   const int32_t t = T > 0 ? T : 1;
-  const int64_t own = sfn::attend_most_parts(R, h_q, kv->h_kv, kv->dtype, e4m3, max_new, own_span(max_own));
-  const int64_t prefix = sfn::attend_most_parts(1, h_q, kv->h_kv, kv->dtype, e4m3, t, max_shared);
+  const int64_t own = sfn::attend_most_parts(R, h_q, kv->h_kv, kv->dtype, max_new, own_span(max_own));
+  const int64_t prefix = sfn::attend_most_parts(1, h_q, kv->h_kv, kv->dtype, t, max_shared);
   return shared_bytes(kv, std::max(own, (int64_t)R * max_new * h_q), std::max(prefix, (int64_t)t * h_q));
 }
 
@@ -691,9 +691,8 @@ int attend_shared(const sfn_kv* kv, const uint8_t* k_exp, const uint8_t* v_exp, 
   if (!aligned16(out)) return SFN_EALIGN;
   for (const int32_t* p : {prefix, shared_len, table, cu, kv_len})
     if (!aligned4_or_null(p)) return SFN_EALIGN;
-  const bool e4m3 = k_exp != nullptr;
-  const sfn::AttendPlan po = sfn::attend_plan(R, h_q, kv->h_kv, kv->dtype, e4m3, max_new, own_span(max_own), 0);
-  const sfn::AttendPlan pp = sfn::attend_plan(1, h_q, kv->h_kv, kv->dtype, e4m3, T, max_shared, 0);
+  const sfn::AttendPlan po = sfn::attend_plan(R, h_q, kv->h_kv, kv->dtype, max_new, own_span(max_own), 0);
+  const sfn::AttendPlan pp = sfn::attend_plan(1, h_q, kv->h_kv, kv->dtype, T, max_shared, 0);
   if ((int64_t)R * po.S * po.row_tiles * kv->h_kv > INT32_MAX || (int64_t)pp.S * pp.row_tiles * kv->h_kv > INT32_MAX) return SFN_ESHAPE;
   const int64_t own_parts = shared_parts((int64_t)R * max_new * h_q, po), prefix_parts = shared_parts((int64_t)T * h_q, pp);
   if ((st = check_ws(ws, ws_bytes, shared_bytes(kv, own_parts, prefix_parts))) != SFN_OK) return st;
@@ -727,7 +726,7 @@ int attend_shared(const sfn_kv* kv, const uint8_t* k_exp, const uint8_t* v_exp, 
 size_t kv_cache_attend_workspace_size(const sfn_kv* kv, int32_t R, int32_t T, int32_t h_q, int32_t max_new,
                                       int32_t max_len) {
   try {
-    return check_kv(kv, false) == SFN_OK ? attend_size(kv, false, R, T, h_q, max_new, max_len) : 0;
+    return check_kv(kv, false) == SFN_OK ? attend_size(kv, R, T, h_q, max_new, max_len) : 0;
   } catch (...) {
     return 0;
   }
@@ -750,7 +749,7 @@ int kv_cache_attend(const sfn_kv* kv, int32_t R, int32_t T, int32_t h_q, const v
 size_t kv8_cache_attend_workspace_size(const sfn_kv8* kv, int32_t R, int32_t T, int32_t h_q, int32_t max_new,
                                        int32_t max_len) {
   try {
-    return check_kv8(kv, false) == SFN_OK ? attend_size(&kv->kv, true, R, T, h_q, max_new, max_len) : 0;
+    return check_kv8(kv, false) == SFN_OK ? attend_size(&kv->kv, R, T, h_q, max_new, max_len) : 0;
   } catch (...) {
     return 0;
   }
@@ -773,7 +772,7 @@ int kv8_cache_attend(const sfn_kv8* kv, int32_t R, int32_t T, int32_t h_q, const
 size_t kv_cache_attend_shared_workspace_size(const sfn_kv* kv, int32_t R, int32_t T, int32_t h_q, int32_t max_new,
                                              int32_t max_shared, int32_t max_own) {
   try {
-    return check_kv(kv, false) == SFN_OK ? shared_size(kv, false, R, T, h_q, max_new, max_shared, max_own) : 0;
+    return check_kv(kv, false) == SFN_OK ? shared_size(kv, R, T, h_q, max_new, max_shared, max_own) : 0;
   } catch (...) {
     return 0;
   }
@@ -797,7 +796,7 @@ int kv_cache_attend_shared(const sfn_kv* kv, int32_t R, int32_t T, int32_t h_q, 
 size_t kv8_cache_attend_shared_workspace_size(const sfn_kv8* kv, int32_t R, int32_t T, int32_t h_q, int32_t max_new,
                                               int32_t max_shared, int32_t max_own) {
   try {
-    return check_kv8(kv, false) == SFN_OK ? shared_size(&kv->kv, true, R, T, h_q, max_new, max_shared, max_own) : 0;
+    return check_kv8(kv, false) == SFN_OK ? shared_size(&kv->kv, R, T, h_q, max_new, max_shared, max_own) : 0;
   } catch (...) {
     return 0;
   }

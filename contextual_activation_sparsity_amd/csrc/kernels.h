@@ -157,9 +157,9 @@ struct AttendPlan {
   int row_tiles, S, chunk;   // workgroups for a key head's rows and for its keys, keys of a split
   int64_t parts;             // rows of partial results
 };
-AttendPlan attend_plan(int R, int h_q, int h_kv, int dtype, bool e4m3, int max_new, int max_len, int window);
+AttendPlan attend_plan(int R, int h_q, int h_kv, int dtype, int max_new, int max_len, int window);
 // Rows of partial results that no call within these bounds passes.
-int64_t attend_most_parts(int R, int h_q, int h_kv, int dtype, bool e4m3, int max_new, int max_len);
+int64_t attend_most_parts(int R, int h_q, int h_kv, int dtype, int max_new, int max_len);
 hipError_t launch_kv_attend(const AttendArgs& a, int dh, int dtype, hipStream_t stream);
 hipError_t launch_kv_attend_shared(const AttendArgs& own, const AttendArgs& prefix, int dh, int dtype, hipStream_t stream);
 

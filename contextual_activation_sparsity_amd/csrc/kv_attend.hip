@@ -84,7 +84,7 @@ struct AttnTile {
   static constexpr bool kBf = WT == WT_BF16, k8 = CT == CT_E4M3;
   static constexpr int KB = kBf ? 2 : 4;           // bytes of a value
   static constexpr int CB = k8 ? 1 : KB;           // and in the cache
-  static constexpr int KT = (kBf ? 32 : 16) * (k8 ? 2 : 1);  // keys of a tile
+  static constexpr int KT = kBf ? 32 : 16;         // keys of a tile
   static constexpr int NG = KT / 16;               // 16-key groups (each within a page)
   static constexpr int NQ = DH * KB / 64;          // 16-byte chunks a lane holds of a row (K, Q)
   static constexpr int VW = (kBf || k8) && DH == 128 ? 8 : 4;  // values a lane reads of a V row
@@ -217,7 +217,7 @@ struct KeyTile {
   uint32_t v[C::NG][4][C::NB][C::VW * C::KB / 4];
 
   // row: the cache row of each group's first key
-  __device__ __forceinline__ void load(const AttendArgs& a, const int64_t (&row)[C::NG], int c, int q) {
+  __device__ __forceinline__ void load_keys(const AttendArgs& a, const int64_t (&row)[C::NG], int c, int q) {
     constexpr int ROW = DH * C::KB;
 #pragma unroll
     for (int u = 0; u < C::NG; ++u) {
@@ -225,6 +225,9 @@ struct KeyTile {
 #pragma unroll
       for (int s = 0; s < C::NQ; ++s) k[u][s] = ldg16(kp + 64 * s);
     }
+  }
+  __device__ __forceinline__ void load_values(const AttendArgs& a, const int64_t (&row)[C::NG], int c, int q) {
+    constexpr int ROW = DH * C::KB;
 #pragma unroll
     for (int u = 0; u < C::NG; ++u) {
       const SFN_GLOBAL char* vp = gp(a.v) + (row[u] + 4 * q) * ROW + c * C::VW * C::KB;
@@ -301,28 +304,33 @@ struct KeyTile<WT, CT_E4M3, DH> {
   uint32_t v[C::NG][4][NV];
   uint32_t kb[C::NG], vb[C::NG];  // the bytes of key c, and of keys 4q .. 4q + 3
 
-  __device__ __forceinline__ void load(const AttendArgs& a, const int64_t (&row)[C::NG], int c, int q) {
+  __device__ __forceinline__ void load_keys(const AttendArgs& a, const int64_t (&row)[C::NG], int c, int q) {
 #pragma unroll
     for (int u = 0; u < C::NG; ++u) {
-      const SFN_GLOBAL char* kp = gp(a.k) + (row[u] + c) * DH + 16 * q;
+      // one address for the wave and an offset for the lane
+      const SFN_GLOBAL char* kp = gp(a.k) + row[u] * DH;
+      const uint32_t at = c * DH + 16 * q;
 #pragma unroll
-      for (int s = 0; s < NR; ++s) k[u][s] = ldg16(kp + 64 * s);
-      kb[u] = gp(a.k_exp)[row[u] + c];
+      for (int s = 0; s < NR; ++s) k[u][s] = ldg16(kp + (at + 64 * s));
+      kb[u] = (gp(a.k_exp) + row[u])[(uint32_t)c];
     }
+  }
+  __device__ __forceinline__ void load_values(const AttendArgs& a, const int64_t (&row)[C::NG], int c, int q) {
 #pragma unroll
     for (int u = 0; u < C::NG; ++u) {
-      const SFN_GLOBAL char* vp = gp(a.v) + (row[u] + 4 * q) * DH + c * C::VW;
+      const SFN_GLOBAL char* vp = gp(a.v) + row[u] * DH;
+      const uint32_t at = 4 * q * DH + c * C::VW;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         if constexpr (NV == 2) {
-          const uint64_t w = __builtin_nontemporal_load(reinterpret_cast<const SFN_GLOBAL uint64_t*>(vp + j * DH));
+          const uint64_t w = __builtin_nontemporal_load(reinterpret_cast<const SFN_GLOBAL uint64_t*>(vp + (at + j * DH)));
           v[u][j][0] = (uint32_t)w;
           v[u][j][1] = (uint32_t)(w >> 32);
         } else {
-          v[u][j][0] = __builtin_nontemporal_load(reinterpret_cast<const SFN_GLOBAL uint32_t*>(vp + j * DH));
+          v[u][j][0] = __builtin_nontemporal_load(reinterpret_cast<const SFN_GLOBAL uint32_t*>(vp + (at + j * DH)));
         }
       }
-      vb[u] = *reinterpret_cast<const SFN_GLOBAL uint32_t*>(gp(a.v_exp) + row[u] + 4 * q);
+      vb[u] = *reinterpret_cast<const SFN_GLOBAL uint32_t*>(gp(a.v_exp) + row[u] + (uint32_t)(4 * q));
     }
   }
 
@@ -341,18 +349,21 @@ struct KeyTile<WT, CT_E4M3, DH> {
   }
 
   __device__ __forceinline__ void add_values(const f32x4_t (&p)[C::NG], f32x4_t (&acc)[C::NO], float& l) const {
-    float scale[C::NG][4];
-#pragma unroll
-    for (int u = 0; u < C::NG; ++u)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) scale[u][j] = scale_of(vb[u] >> (8 * j) & 0xffu);
     if constexpr (C::kBf) {
 #pragma unroll
       for (int u = 0; u < C::NG; u += 2) {
         // rounded to bf16, and their sum, as in add_weighted
-        const uint4 pw = make_uint4(pack_bf16(p[u][0], p[u][1]), pack_bf16(p[u][2], p[u][3]), pack_bf16(p[u + 1][0], p[u + 1][1]),
+        uint4 pw = make_uint4(pack_bf16(p[u][0], p[u][1]), pack_bf16(p[u][2], p[u][3]), pack_bf16(p[u + 1][0], p[u + 1][1]),
                                     pack_bf16(p[u + 1][2], p[u + 1][3]));
         l = add_pair(pw.x, add_pair(pw.y, l)) + add_pair(pw.z, add_pair(pw.w, 0.f));
+        float scale[2][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t b = vb[u + h];
+          asm("" : "+v"(b), "+v"(pw.w));  // not before the weights are there: turned values take four times the registers
+#pragma unroll
+          for (int j = 0; j < 4; ++j) scale[h][j] = scale_of(b >> (8 * j) & 0xffu);
+        }
 #pragma unroll
         for (int e = 0; e < C::VW; e += 2) {
           uint32_t x[2][4];  // values e and e + 1 of the lane's eight keys
@@ -360,7 +371,7 @@ struct KeyTile<WT, CT_E4M3, DH> {
           for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-              x[h][j] = e & 2 ? pair_of<true>(v[u + h][j][e >> 2], scale[u + h][j]) : pair_of<false>(v[u + h][j][e >> 2], scale[u + h][j]);
+              x[h][j] = e & 2 ? pair_of<true>(v[u + h][j][e >> 2], scale[h][j]) : pair_of<false>(v[u + h][j][e >> 2], scale[h][j]);
 #pragma unroll
           for (int o = 0; o < 2; ++o) {
             const uint32_t sel = o ? 0x07060302u : 0x05040100u;
@@ -380,7 +391,7 @@ struct KeyTile<WT, CT_E4M3, DH> {
 #pragma unroll
           for (int e = 0; e < C::VW; e += 4) {
             float f[4];
-            values_of(v[u][j][e >> 2], scale[u][j], f);
+            values_of(v[u][j][e >> 2], scale_of(vb[u] >> (8 * j) & 0xffu), f);
 #pragma unroll
             for (int o = 0; o < 4; ++o) acc[e + o] = __builtin_amdgcn_mfma_f32_16x16x4f32(f[o], p[u][j], acc[e + o], 0, 0, 0);
           }
@@ -406,7 +417,11 @@ struct KeyTile<WT, CT_E4M3, DH> {
 #pragma unroll
       for (int j = 0; j < 4; ++j)
 #pragma unroll
-        for (int w = 0; w < NV; ++w) v[u][j][w] = without_nan(v[u][j][w]);
+        for (int w = 0; w < NV; ++w) {
+          uint32_t& x = v[u][j][w];
+          asm("" : "+v"(x));  // opaque, so that nothing of the first pass is kept for this rare one
+          x = without_nan(x);
+        }
     return true;
   }
 };
@@ -470,11 +485,15 @@ __global__ __launch_bounds__(64 * NW, NW == 8 || RT == 2 ? 2 : 3) void attend_sp
     for (int u = 0; u < NG; ++u) page[u] = page_of(kt + 16 * u);
   };
   // the tile at kt, from the pages found for it, and then the pages of the one after it
-  auto fetch = [&](int kt) {
-    int64_t row[NG];
+  int64_t row[NG];
+  auto place = [&](int kt) {
 #pragma unroll
     for (int u = 0; u < NG; ++u) row[u] = row_in(page[u], kt + 16 * u);
-    tile.load(a, row, c, q);
+  };
+  auto fetch = [&](int kt) {
+    place(kt);
+    tile.load_keys(a, row, c, q);
+    tile.load_values(a, row, c, q);
     if (kt + NW * KT < k1) find(kt + NW * KT);
   };
   if (kw < k1) {
@@ -506,78 +525,104 @@ __global__ __launch_bounds__(64 * NW, NW == 8 || RT == 2 ? 2 : 3) void attend_sp
     for (int o = 0; o < NO; ++o) acc[x][o] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   }
 
-  for (int kt = kw; kt < k1;) {
-    // A masked key has weight 0, but 0 times a value that is not finite is NaN: a tile with a
-    // masked key and such a value takes the long way below, so that no token's result
-    // depends on tokens it does not see.
-    const bool full = kt >= lo_all && kt + KT <= hi_all;  // every row sees every key of the tile
-    const bool odd = full ? false : tile.clean(len - kt, q);
+  auto scores = [&](int x, f32x4_t (&s)[NG]) __attribute__((always_inline)) {
 #pragma unroll
-    for (int x = 0; x < RT; ++x) {
-      f32x4_t s[NG];
+    for (int u = 0; u < NG; ++u) {
+      const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
+      if constexpr (C::kBf) {
+        s[u] = zero;
 #pragma unroll
-      for (int u = 0; u < NG; ++u) {
-        const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
-        if constexpr (C::kBf) {
-          s[u] = zero;
+        for (int i = 0; i < NQ; ++i)
+          s[u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, tile.key_chunk(u, i)),
+                                                         __builtin_bit_cast(bf16x8_t, qf[x][i]), s[u], 0, 0, 0);
+      } else {
+        // four sums side by side: half the rounding error of one chain of dh additions (sharp
+        // scores, 600 keys: 4.4e-7 of the result against 1.1e-6), for 10.0 instead of 9.8 us
+        // of the windowed fp32 chunk
+        f32x4_t part[4] = {zero, zero, zero, zero};
 #pragma unroll
-          for (int i = 0; i < NQ; ++i)
-            s[u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, tile.key_chunk(u, i)),
-                                                           __builtin_bit_cast(bf16x8_t, qf[x][i]), s[u], 0, 0, 0);
-        } else {
-          // four sums side by side: half the rounding error of one chain of dh additions (sharp
-          // scores, 600 keys: 4.4e-7 of the result against 1.1e-6), for 10.0 instead of 9.8 us
-          // of the windowed fp32 chunk
-          f32x4_t part[4] = {zero, zero, zero, zero};
+        for (int i = 0; i < NQ; ++i) {
+          const f32x4_t kk = __builtin_bit_cast(f32x4_t, tile.key_chunk(u, i)), qq = __builtin_bit_cast(f32x4_t, qf[x][i]);
 #pragma unroll
-          for (int i = 0; i < NQ; ++i) {
-            const f32x4_t kk = __builtin_bit_cast(f32x4_t, tile.key_chunk(u, i)), qq = __builtin_bit_cast(f32x4_t, qf[x][i]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) part[e] = __builtin_amdgcn_mfma_f32_16x16x4f32(kk[e], qq[e], part[e], 0, 0, 0);
-          }
-          s[u] = (part[0] + part[1]) + (part[2] + part[3]);
+          for (int e = 0; e < 4; ++e) part[e] = __builtin_amdgcn_mfma_f32_16x16x4f32(kk[e], qq[e], part[e], 0, 0, 0);
         }
-      }
-      // p = 2^(scale s - m), scale and m in units of log2, with one rounding
-      float top = kNegInf;
-#pragma unroll
-      for (int u = 0; u < NG; ++u)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (!full) {
-            const int key = 16 * u + i, at = kt + 4 * q;
-            s[u][i] = key < row_hi[x] - at && key >= row_lo[x] - at ? s[u][i] : kNegInf;
-          }
-          top = fmaxf(top, s[u][i]);
-        }
-      top = swap_pair_max<16>(top);
-      top = swap_pair_max<32>(top) * a.scale_log2;  // the scale is positive
-      const float mn = fmaxf(m[x], top);
-      const float ms = mn == kNegInf ? 0.f : mn;
-      if (__any(mn > m[x])) {
-        const float al = exp2_f(m[x] - ms);
-        l[x] *= al;
-#pragma unroll
-        for (int o = 0; o < NO; ++o)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[x][o][i] *= al;
-        m[x] = mn;
-      }
-#pragma unroll
-      for (int u = 0; u < NG; ++u)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s[u][i] = exp2_f(fmaf(s[u][i], a.scale_log2, -ms));
-      tile.add_values(s, acc[x], l[x]);
-      if (odd) {
-        // the values that are not finite: key by key, read again, into the rows that see them
-#pragma unroll 1
-        for (int kk = 0; kk < KT && kt + kk < len; ++kk)
-          add_one_key<WT, CT, DH>(gp(a.v) + ((row_in(page_of(kt + kk), kt + kk) + (kk & 15)) * DH + c * VW) * C::CB, s, kk, q,
-                                  kt + kk < row_hi[x] && kt + kk >= row_lo[x], acc[x]);
+        s[u] = (part[0] + part[1]) + (part[2] + part[3]);
       }
     }
-    kt += NW * KT;
-    if (kt < k1) fetch(kt);
+  };
+  auto weigh = [&](int x, f32x4_t (&s)[NG], int kt, bool full, bool odd) __attribute__((always_inline)) {
+    // p = 2^(scale s - m), scale and m in units of log2, with one rounding
+    float top = kNegInf;
+#pragma unroll
+    for (int u = 0; u < NG; ++u)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (!full) {
+          const int key = 16 * u + i, at = kt + 4 * q;
+          s[u][i] = key < row_hi[x] - at && key >= row_lo[x] - at ? s[u][i] : kNegInf;
+        }
+        top = fmaxf(top, s[u][i]);
+      }
+    top = swap_pair_max<16>(top);
+    top = swap_pair_max<32>(top) * a.scale_log2;  // the scale is positive
+    const float mn = fmaxf(m[x], top);
+    const float ms = mn == kNegInf ? 0.f : mn;
+    if (__any(mn > m[x])) {
+      const float al = exp2_f(m[x] - ms);
+      l[x] *= al;
+#pragma unroll
+      for (int o = 0; o < NO; ++o)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[x][o][i] *= al;
+      m[x] = mn;
+    }
+#pragma unroll
+    for (int u = 0; u < NG; ++u)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[u][i] = exp2_f(fmaf(s[u][i], a.scale_log2, -ms));
+    tile.add_values(s, acc[x], l[x]);
+    if (odd) {
+      // the values that are not finite: key by key, read again, into the rows that see them
+#pragma unroll 1
+      for (int kk = 0; kk < KT && kt + kk < len; ++kk)
+        add_one_key<WT, CT, DH>(gp(a.v) + ((row_in(page_of(kt + kk), kt + kk) + (kk & 15)) * DH + c * VW) * C::CB, s, kk, q,
+                                kt + kk < row_hi[x] && kt + kk >= row_lo[x], acc[x]);
+    }
+  };
+  for (int kt = kw; kt < k1;) {
+    const bool full = kt >= lo_all && kt + KT <= hi_all;  // every row sees every key of the tile
+    const int next = kt + NW * KT;
+    // A masked key has weight 0, but 0 times a value that is not finite is NaN: a tile with a
+    // masked key and such a value takes the long way in weigh(), so that no token's result
+    // depends on tokens it does not see.
+    if constexpr (C::k8) {
+      // turning codes into values takes more time than the products, so the loads are under way
+      // meanwhile: the next tile's keys from here on, its values after this one's
+      f32x4_t s[RT][NG];
+#pragma unroll
+      for (int x = 0; x < RT; ++x) scores(x, s[x]);
+      if (next < k1) {
+        place(next);
+        tile.load_keys(a, row, c, q);
+      }
+      const bool odd = full ? false : tile.clean(len - kt, q);
+#pragma unroll
+      for (int x = 0; x < RT; ++x) weigh(x, s[x], kt, full, odd);
+      if (next < k1) {
+        tile.load_values(a, row, c, q);
+        if (next + NW * KT < k1) find(next + NW * KT);
+      }
+    } else {
+      const bool odd = full ? false : tile.clean(len - kt, q);
+#pragma unroll
+      for (int x = 0; x < RT; ++x) {
+        f32x4_t s[NG];
+        scores(x, s);
+        weigh(x, s, kt, full, odd);
+      }
+      if (next < k1) fetch(next);
+    }
+    kt = next;
   }
 
   // join the waves: a common maximum, then the sums in wave order
@@ -1326,12 +1371,12 @@ void by_type(int dh, int dtype, bool e4m3, F f) {
 //     1016 keys 20.5 and 23.2; a prompt of 400 tokens, 32 / 8 heads, 22.2 and 14.8.
 constexpr int kPartsOfRound = 6500, kPartsOfJoin = 10000;
 constexpr int kFill = 512, kLeast = 128, kMost = 3200, kWhole = 384;
-AttendPlan attend_plan(int R, int h_q, int h_kv, int dtype, bool e4m3, int max_new, int max_len, int window) {
+AttendPlan attend_plan(int R, int h_q, int h_kv, int dtype, int max_new, int max_len, int window) {
   AttendPlan p{};
   const int64_t rows = (int64_t)max_new * (h_q / h_kv);
   const bool bf = dtype == SFN_BF16;
   p.tile_rows = rows <= 16 ? 16 : rows <= 32 || !bf ? 32 : kTileRows;
-  p.tile_keys = p.tile_rows == kTileRows ? kTileKeys : (bf ? 32 : 16) * (e4m3 ? 2 : 1);
+  p.tile_keys = p.tile_rows == kTileRows ? kTileKeys : bf ? 32 : 16;
   p.row_tiles = (int)((rows + p.tile_rows - 1) / p.tile_rows);
   const int64_t base = (int64_t)R * h_kv * p.row_tiles;
   const bool tile = p.tile_rows == kTileRows;
@@ -1361,7 +1406,7 @@ AttendPlan attend_plan(int R, int h_q, int h_kv, int dtype, bool e4m3, int max_n
 // kMost of several requests; kTileFill of the tile kernel), each with a tile's rows of parts; nor
 // can a row have more splits than its keys have steps. More new tokens may mean fewer parts (up
 // to none), so this is taken over all calls within the bounds.
-int64_t attend_most_parts(int R, int h_q, int h_kv, int dtype, bool e4m3, int max_new, int max_len) {
+int64_t attend_most_parts(int R, int h_q, int h_kv, int dtype, int max_new, int max_len) {
   const bool bf = dtype == SFN_BF16;
   const int g = h_q / h_kv;
   auto parts = [&](int64_t tokens, int64_t keys, int64_t step, int64_t rows_launched) {
@@ -1369,7 +1414,7 @@ int64_t attend_most_parts(int R, int h_q, int h_kv, int dtype, bool e4m3, int ma
     return s > 1 ? std::min((int64_t)R * tokens * h_q * s, rows_launched) : 0;
   };
   const int64_t split = max_len <= kWhole ? 0
-                                          : parts(bf ? std::min(max_new, 32 / g) : max_new, max_len, 4 * (bf ? 32 : 16) * (e4m3 ? 2 : 1),
+                                          : parts(bf ? std::min(max_new, 32 / g) : max_new, max_len, 4 * (bf ? 32 : 16),
                                                   32 * (R > 1 ? std::max(2 * kFill, kMost) : 2 * kFill));
   const int64_t tile = bf && (int64_t)max_new * g > 32 ? parts(max_new, max_len, kTileKeys, (int64_t)kTileRows * kTileFill) : 0;
   return std::max(split, tile);
