@@ -621,6 +621,7 @@ void set_plan(sfn::AttendArgs& a, const sfn::AttendPlan& p, const sfn_kv* kv, ch
   a.row_tiles = p.row_tiles;
   a.S = p.S;
   a.chunk = p.chunk;
+  a.groups = p.groups;
 }
 
 int attend(const sfn_kv* kv, const uint8_t* k_exp, const uint8_t* v_exp, int32_t R, int32_t T, int32_t h_q, const void* q, int64_t q_stride,
@@ -647,9 +648,6 @@ int attend(const sfn_kv* kv, const uint8_t* k_exp, const uint8_t* v_exp, int32_t
   a.max_new = max_new;
   a.max_len = max_len;
   a.window = window;
-  a.kind = sfn::ATTEND_PLAIN;
-  a.cu_step = 1;
-  a.whole = p.S == 1;
   return hip_status(sfn::launch_kv_attend(a, kv->dh, kv->dtype, static_cast<hipStream_t>(stream)));
 }
 
@@ -672,7 +670,7 @@ size_t shared_size(const sfn_kv* kv, int32_t R, int32_t T, int32_t h_q, int32_t 
   if (check_shared(kv, R, T, h_q, max_new, max_shared, max_own) != SFN_OK) return 0;
   const int32_t t = T > 0 ? T : 1;
   const int64_t own = sfn::attend_most_parts(R, h_q, kv->h_kv, kv->dtype, max_new, own_span(max_own));
-  const int64_t prefix = sfn::attend_most_parts(1, h_q, kv->h_kv, kv->dtype, t, max_shared);
+  const int64_t prefix = sfn::prefix_most_parts(t, h_q, kv->h_kv, kv->dtype, max_shared);
   return shared_bytes(kv, std::max(own, (int64_t)R * max_new * h_q), std::max(prefix, (int64_t)t * h_q));
 }
 
@@ -692,7 +690,7 @@ int attend_shared(const sfn_kv* kv, const uint8_t* k_exp, const uint8_t* v_exp, 
   for (const int32_t* p : {prefix, shared_len, table, cu, kv_len})
     if (!aligned4_or_null(p)) return SFN_EALIGN;
   const sfn::AttendPlan po = sfn::attend_plan(R, h_q, kv->h_kv, kv->dtype, max_new, own_span(max_own), 0);
-  const sfn::AttendPlan pp = sfn::attend_plan(1, h_q, kv->h_kv, kv->dtype, T, max_shared, 0);
+  const sfn::AttendPlan pp = sfn::prefix_plan(T, h_q, kv->h_kv, kv->dtype, max_shared);
   if ((int64_t)R * po.S * po.row_tiles * kv->h_kv > INT32_MAX || (int64_t)pp.S * pp.row_tiles * kv->h_kv > INT32_MAX) return SFN_ESHAPE;
   const int64_t own_parts = shared_parts((int64_t)R * max_new * h_q, po), prefix_parts = shared_parts((int64_t)T * h_q, pp);
   if ((st = check_ws(ws, ws_bytes, shared_bytes(kv, own_parts, prefix_parts))) != SFN_OK) return st;

@@ -25,24 +25,26 @@ enum { CT_SAME = 0, CT_E4M3 = 1 };
 // the prefix takes all tokens as one request, all of which see every key of it (past = len);
 // the part over the rest starts behind the prefix for a request whose tokens all come after it,
 // and otherwise reads everything from the request's own pages.
+template <bool SHARED>
 struct Request {
   int t0, n, len, past, from;
   __device__ __forceinline__ Request(const AttendArgs& a, int r) {
-    t0 = min(max(gp(a.cu)[r], 0), a.T);
-    n = min(max(gp(a.cu)[r + a.cu_step], t0), a.T) - t0;
+    // every word is read at once: a read that waits for another is a microsecond of a short call
+    const int c0 = gp(a.cu)[r], c1 = gp(a.cu)[r + (SHARED ? a.cu_step : 1)], kl = gp(a.kv_len)[r];
+    t0 = min(max(c0, 0), a.T);
+    n = min(max(c1, t0), a.T) - t0;
+    len = min(max(kl, 0), a.max_len);
     from = 0;
-    if (a.kind == ATTEND_PREFIX) {
-      past = len = min(max(gp(a.shared)[0], 0), a.max_len);
-      return;
-    }
-    len = min(max(gp(a.kv_len)[r], 0), a.max_len);
-    if (a.kind == ATTEND_OWN) {
-      const int shared = shared_len(a);
-      len = min(len, shared + a.max_own);
-      if (len - n >= shared) from = shared;
-      else len = min(len, a.max_own);
-    }
     past = len - n;
+    if constexpr (SHARED) {
+      const int shared = shared_len(a);
+      int own = min(len, shared + a.max_own);
+      const bool after = own - n >= shared;
+      own = after ? own : min(own, a.max_own);
+      len = a.kind == ATTEND_PREFIX ? min(shared, a.max_len) : own;
+      past = a.kind == ATTEND_PREFIX ? len : own - n;
+      from = a.kind == ATTEND_OWN && after ? shared : 0;
+    }
   }
   __device__ __forceinline__ static int shared_len(const AttendArgs& a) { return min(max(gp(a.shared)[0], 0), a.max_shared); }
 };
@@ -438,7 +440,7 @@ struct RowMap {
   __device__ __forceinline__ int head(int i, int tok) const { return i + rem0 - (tok - tok0) * g; }
 };
 
-template <int WT, int CT, int DH, int RT, int NW>
+template <int WT, int CT, int DH, int RT, int NW, bool SHARED>
 __global__ __launch_bounds__(64 * NW, NW == 8 || RT == 2 ? 2 : 3) void attend_split_kernel(AttendArgs a) {
   using C = AttnTile<WT, CT, DH>;
   constexpr int KT = C::KT, NG = C::NG, NQ = C::NQ, VW = C::VW, NB = C::NB, NO = C::NO, KB = C::KB;
@@ -463,7 +465,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 || RT == 2 ? 2 : 3) void attend_sp
 #pragma unroll
   for (int u = 0; u < NG; ++u) page[u] = page_of(split * a.chunk + wave * KT + 16 * u);
 
-  const Request req(a, r);
+  const Request<SHARED> req(a, r);
   const int t0 = req.t0, len = req.len, past = req.past;
   const int g = a.g, rows = min(req.n, a.max_new) * g;
   const int rho0 = rtile * TR;
@@ -472,9 +474,9 @@ __global__ __launch_bounds__(64 * NW, NW == 8 || RT == 2 ? 2 : 3) void attend_sp
   const int last = min(TR, rows - rho0) - 1, tok1 = map.token(last);
   // keys that some row of the tile sees, and that every row sees
   const int hi = max(0, min(past + tok1 + 1, len));
-  const int lo = a.window > 0 ? max(0, past + map.tok0 + 1 - a.window) : req.from;
+  const int lo = a.window > 0 ? max(0, past + map.tok0 + 1 - a.window) : SHARED ? req.from : 0;
   const int hi_all = min(past + map.tok0 + 1, len);
-  const int lo_all = a.window > 0 ? max(0, past + tok1 + 1 - a.window) : req.from;
+  const int lo_all = a.window > 0 ? max(0, past + tok1 + 1 - a.window) : SHARED ? req.from : 0;
   const int k0 = (lo & ~(KT - 1)) + split * a.chunk, k1 = min(k0 + a.chunk, hi);
   if (split > 0 && k0 >= hi) return;
 
@@ -512,7 +514,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 || RT == 2 ? 2 : 3) void attend_sp
 #pragma unroll
     for (int s = 0; s < NQ; ++s) qf[x][s] = ld16(src + C::chunk_at(s, q) * KB);
     row_hi[x] = ok ? min(past + tok + 1, len) : 0;
-    row_lo[x] = a.window > 0 ? past + tok + 1 - a.window : req.from;
+    row_lo[x] = a.window > 0 ? past + tok + 1 - a.window : SHARED ? req.from : 0;
   }
 
   f32x4_t acc[RT][NO];
@@ -661,7 +663,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 || RT == 2 ? 2 : 3) void attend_sp
       L += s_l[w][x];
       o += *reinterpret_cast<const f32x4_t*>(&s_o[w][x][d4]);
     }
-    if (a.whole) {
+    if (SHARED ? false : a.S == 1) {
       store_row<WT, DH>(a, t0 + tok, head, d4, o, L);
     } else {
       const int64_t at = (((int64_t)r * a.max_new + tok) * a.h_q + head) * a.S + split;
@@ -915,7 +917,7 @@ struct CodeRows {
 // KG groups of four waves: with two of them (a split of the keys for few row tiles) each takes
 // every second stage, with buffers of its own, and the groups join in LDS at the end, so that
 // there are half as many parts to write and join as with two workgroups.
-template <int CT, int DH, int KG>
+template <int CT, int DH, int KG, bool SHARED>
 __global__ __launch_bounds__(256 * KG, 2) void attend_tile_kernel(AttendArgs a) {
   using W = TileWave<CT, DH>;
   constexpr bool k8 = CT == CT_E4M3;
@@ -946,7 +948,7 @@ __global__ __launch_bounds__(256 * KG, 2) void attend_tile_kernel(AttendArgs a) 
   // without a window the first stage does not depend on the lengths: its page is read with them
   int page = page_of(split * a.chunk + kg * KT);
 
-  const Request req(a, r);
+  const Request<SHARED> req(a, r);
   const int t0 = req.t0, len = req.len, past = req.past;
   const int g = a.g, rows = min(req.n, a.max_new) * g;
   const int rho0 = rtile * kTileRows;
@@ -956,9 +958,9 @@ __global__ __launch_bounds__(256 * KG, 2) void attend_tile_kernel(AttendArgs a) 
   // keys that some row of the tile sees, and that every row sees
   const int tok1 = map.token(last);
   const int hi = max(0, min(past + tok1 + 1, len));
-  const int lo = a.window > 0 ? max(0, past + map.tok0 + 1 - a.window) : req.from;
+  const int lo = a.window > 0 ? max(0, past + map.tok0 + 1 - a.window) : SHARED ? req.from : 0;
   const int tile_hi = min(past + map.tok0 + 1, len);
-  const int tile_lo = a.window > 0 ? past + tok1 + 1 - a.window : req.from;
+  const int tile_lo = a.window > 0 ? past + tok1 + 1 - a.window : SHARED ? req.from : 0;
   const int k0 = (lo & ~(KT - 1)) + split * a.chunk, k1 = min(k0 + a.chunk, hi);
   if (split > 0 && k0 >= hi) return;
 
@@ -988,13 +990,13 @@ __global__ __launch_bounds__(256 * KG, 2) void attend_tile_kernel(AttendArgs a) 
   const int i0 = 32 * wave, i1 = min(i0 + 31, last);  // none if i0 > last
   const int wt0 = map.token(i0), wt1 = map.token(max(i1, 0));
   const int some_hi = i0 <= last ? min(past + wt1 + 1, len) : 0;  // keys that some row of it sees
-  const int some_lo = a.window > 0 ? past + wt0 + 1 - a.window : req.from;
+  const int some_lo = a.window > 0 ? past + wt0 + 1 - a.window : SHARED ? req.from : 0;
   const int all_hi = min(past + wt0 + 1, len);  // and that every row sees
-  const int all_lo = a.window > 0 ? past + wt1 + 1 - a.window : req.from;
+  const int all_lo = a.window > 0 ? past + wt1 + 1 - a.window : SHARED ? req.from : 0;
   const bool ok = i0 + c <= last;
   const int i = ok ? i0 + c : 0, tok = map.token(i), head = hk * g + map.head(i, tok);
   w.row_hi = ok ? min(past + tok + 1, len) : 0;
-  w.row_lo = a.window > 0 ? past + tok + 1 - a.window : req.from;
+  w.row_lo = a.window > 0 ? past + tok + 1 - a.window : SHARED ? req.from : 0;
   w.m = kNegInf;
   w.l = 0.f;
   {
@@ -1086,7 +1088,7 @@ __global__ __launch_bounds__(256 * KG, 2) void attend_tile_kernel(AttendArgs a) 
   // every 8 of its row). 16-byte places are permuted like the stages'.
   constexpr int OC = DH / 4;  // 16-byte places of an fp32 row
   char* const out = KG == 1 ? (wave < 2 ? s_a : s_b) + (wave & 1) * 32 * DH * 4 : s_a + wave * 32 * DH * 4;
-  const bool whole = a.whole;
+  const bool whole = !SHARED && a.S == 1;
   const float inv = whole ? (l == 0.f ? 0.f : 1.0f / l) : 1.f;
 #pragma unroll
   for (int d = 0; d < ND; ++d)
@@ -1117,11 +1119,12 @@ __global__ __launch_bounds__(256 * KG, 2) void attend_tile_kernel(AttendArgs a) 
 
 // The splits that wrote parts of the row of token i and head `head` of a request: those of the
 // keys that some row of its row tile saw. At most S.
-__device__ __forceinline__ int splits_used(const AttendArgs& a, const Request& req, int i, int head) {
+template <bool SHARED>
+__device__ __forceinline__ int splits_used(const AttendArgs& a, const Request<SHARED>& req, int i, int head) {
   const int g = a.g, rho0 = (i * g + head % g) / a.tile_rows * a.tile_rows;
   const int rho1 = min(rho0 + a.tile_rows, min(req.n, a.max_new) * g) - 1;
   const int hi = max(0, min(req.past + rho1 / g + 1, req.len));
-  const int lo = a.window > 0 ? max(0, req.past + rho0 / g + 1 - a.window) : req.from;
+  const int lo = a.window > 0 ? max(0, req.past + rho0 / g + 1 - a.window) : SHARED ? req.from : 0;
   const int span = hi - (lo & ~(a.tile_keys - 1));
   return span > 0 ? (span + a.chunk - 1) / a.chunk : 1;
 }
@@ -1150,7 +1153,7 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a) {
 #pragma unroll
   for (int u = 0; u < U; ++u) v[u] = src[(int64_t)min(s0 + u * NS, a.S - 1) * LD];
 
-  const Request req(a, r);
+  const Request<false> req(a, r);
   if (i >= req.n) return;
   const int t0 = req.t0, used = splits_used(a, req, i, head);
 
@@ -1207,9 +1210,9 @@ __global__ __launch_bounds__(256) void attend_join_shared_kernel(AttendArgs a, A
   const int i = blockIdx.x, r = blockIdx.z, head = WAVE ? blockIdx.y * 4 + wave : blockIdx.y;
   if (WAVE && head >= a.h_q) return;
   float* const w_of = s_w[WAVE ? wave : 0];
-  const Request req(a, r);
+  const Request<true> req(a, r);
   if (i >= req.n) return;
-  const int shared = Request::shared_len(a);
+  const int shared = Request<true>::shared_len(a);
   const int first = min(max(gp(a.cu)[0], 0), a.T);  // the prefix's parts begin with this token
   const int mine = splits_used(a, req, i, head);
   const int all = mine + (req.past >= shared ? (shared + p.chunk - 1) / p.chunk : 0);
@@ -1288,7 +1291,7 @@ constexpr int kJoinByWave = 512;
 // items 15.5 with 8, 13.8 with 4 (three workgroups to a compute unit then), 4096 items 92 and 63.
 constexpr int kWideMost = 256;
 
-template <int WT, int CT, int DH>
+template <int WT, int CT, int DH, bool SHARED>
 void launch_parts(const AttendArgs& a, hipStream_t stream) {
   // heads first: the row tiles of a key head lie a multiple of h_kv apart, so that with 8 (or
   // 16, ...) key heads they share an XCD's L2
@@ -1299,24 +1302,24 @@ void launch_parts(const AttendArgs& a, hipStream_t stream) {
   const dim3 grid(a.row_tiles * a.h_kv, a.S | 1, a.R), block(256);
   if (a.tile_rows == kTileRows) {
     if constexpr (WT == WT_BF16) {
-      if ((int64_t)a.R * a.S * a.row_tiles * a.h_kv > kTileFill)
-        hipLaunchKernelGGL((attend_tile_kernel<CT, DH, 1>), grid, block, 0, stream, a);
-      else hipLaunchKernelGGL((attend_tile_kernel<CT, DH, 2>), grid, dim3(512), 0, stream, a);
+      if (a.groups == 1)
+        hipLaunchKernelGGL((attend_tile_kernel<CT, DH, 1, SHARED>), grid, block, 0, stream, a);
+      else hipLaunchKernelGGL((attend_tile_kernel<CT, DH, 2, SHARED>), grid, dim3(512), 0, stream, a);
     }
   } else {
     // one workgroup for all of an item's keys and a compute unit for each: more waves
     const bool wide = a.S == 1 && (int64_t)a.R * a.row_tiles * a.h_kv <= kWideMost;
     const dim3 threads(wide ? 512 : 256);
-    if (a.tile_rows == 16 && wide) hipLaunchKernelGGL((attend_split_kernel<WT, CT, DH, 1, 8>), grid, threads, 0, stream, a);
-    else if (a.tile_rows == 16) hipLaunchKernelGGL((attend_split_kernel<WT, CT, DH, 1, 4>), grid, threads, 0, stream, a);
-    else if (wide) hipLaunchKernelGGL((attend_split_kernel<WT, CT, DH, 2, 8>), grid, threads, 0, stream, a);
-    else hipLaunchKernelGGL((attend_split_kernel<WT, CT, DH, 2, 4>), grid, threads, 0, stream, a);
+    if (a.tile_rows == 16 && wide) hipLaunchKernelGGL((attend_split_kernel<WT, CT, DH, 1, 8, SHARED>), grid, threads, 0, stream, a);
+    else if (a.tile_rows == 16) hipLaunchKernelGGL((attend_split_kernel<WT, CT, DH, 1, 4, SHARED>), grid, threads, 0, stream, a);
+    else if (wide) hipLaunchKernelGGL((attend_split_kernel<WT, CT, DH, 2, 8, SHARED>), grid, threads, 0, stream, a);
+    else hipLaunchKernelGGL((attend_split_kernel<WT, CT, DH, 2, 4, SHARED>), grid, threads, 0, stream, a);
   }
 }
 
 template <int WT, int CT, int DH>
 void launch_sized(const AttendArgs& a, hipStream_t stream) {
-  launch_parts<WT, CT, DH>(a, stream);
+  launch_parts<WT, CT, DH, false>(a, stream);
   if (a.S > 1) {
     if (a.S <= 64 && (int64_t)a.R * a.max_new * a.h_q >= kJoinByWave)
       hipLaunchKernelGGL((attend_join_kernel<WT, DH, true>), dim3(a.max_new, (a.h_q + 3) / 4, a.R), dim3(256), 0, stream, a);
@@ -1327,8 +1330,8 @@ void launch_sized(const AttendArgs& a, hipStream_t stream) {
 
 template <int WT, int CT, int DH>
 void launch_shared(const AttendArgs& own, const AttendArgs& prefix, hipStream_t stream) {
-  launch_parts<WT, CT, DH>(prefix, stream);
-  launch_parts<WT, CT, DH>(own, stream);
+  launch_parts<WT, CT, DH, true>(prefix, stream);
+  launch_parts<WT, CT, DH, true>(own, stream);
   if ((int64_t)own.R * own.max_new * own.h_q >= kJoinByWave)
     hipLaunchKernelGGL((attend_join_shared_kernel<WT, DH, true>), dim3(own.max_new, (own.h_q + 3) / 4, own.R), dim3(256), 0, stream, own, prefix);
   else
@@ -1399,6 +1402,7 @@ AttendPlan attend_plan(int R, int h_q, int h_kv, int dtype, int max_new, int max
   p.chunk = (int)chunk;
   p.S = (int)((span + chunk - 1) / chunk);
   p.parts = p.S > 1 ? (int64_t)R * max_new * h_q * p.S : 0;
+  p.groups = (int64_t)base * p.S > kTileFill ? 1 : 2;
   return p;
 }
 
@@ -1418,6 +1422,43 @@ int64_t attend_most_parts(int R, int h_q, int h_kv, int dtype, int max_new, int 
                                                   32 * (R > 1 ? std::max(2 * kFill, kMost) : 2 * kFill));
   const int64_t tile = bf && (int64_t)max_new * g > 32 ? parts(max_new, max_len, kTileKeys, (int64_t)kTileRows * kTileFill) : 0;
   return std::max(split, tile);
+}
+
+#ifndef T_KG
+#define T_KG 0
+#define T_ROUNDS 4
+#endif
+// The prefix that all tokens of a call share. Its keys are the same for every row tile, so the tile
+// kernel's splits can be chosen to fill the chip evenly: ...
+constexpr int kPrefixRounds = T_ROUNDS;
+AttendPlan prefix_plan(int T, int h_q, int h_kv, int dtype, int max_shared) {
+  AttendPlan p = attend_plan(1, h_q, h_kv, dtype, T, max_shared, 0);
+  if (p.tile_rows != kTileRows) return p;
+  const int64_t base = (int64_t)h_kv * p.row_tiles, span = std::max(1, max_shared), rows = (int64_t)T * h_q;
+  auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
+  double best = 0;
+  for (int k = 0; k <= kPrefixRounds; ++k) {
+    const int64_t s = k ? std::min<int64_t>(k * kTileFill / base, kMaxSplits) : 1;
+    if (s < 1) continue;
+    const int64_t chunk = up(up(span, s), kTileKeys) * kTileKeys, S = up(span, chunk), n = base * S;
+    for (int g = 1; g <= 2; ++g) {
+      if (T_KG && g != T_KG) continue;
+      const double cost = (g == 2 ? up(n, 256) * up(chunk, 2 * kTileKeys) : up(n, 512) * up(chunk, kTileKeys)) + (double)(rows * S) / kPartsOfRound;
+      if (best == 0 || cost < best) {
+        best = cost;
+        p.chunk = (int)chunk;
+        p.S = (int)S;
+        p.groups = g;
+      }
+    }
+  }
+  return p;
+}
+
+int64_t prefix_most_parts(int T, int h_q, int h_kv, int dtype, int max_shared) {
+  const int64_t rows = (int64_t)T * h_q, other = attend_most_parts(1, h_q, h_kv, dtype, T, max_shared);
+  const int64_t splits = std::min<int64_t>((max_shared + kTileKeys - 1) / kTileKeys, kMaxSplits);
+  return std::max({rows, other, std::min(rows * std::max<int64_t>(splits, 1), (int64_t)kTileRows * kTileFill * kPrefixRounds)});
 }
 
 hipError_t launch_kv_attend(const AttendArgs& a, int dh, int dtype, hipStream_t stream) {
