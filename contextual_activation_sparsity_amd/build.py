@@ -37,7 +37,7 @@ SAN_BUILD = os.path.join(BUILD, "san")
 SAN_LIB = os.path.join(SAN_BUILD, "libsparse_ffn_san.so")
 
 SOURCES = ["api.cpp", "decode.hip", "svd_predict.hip", "dense_chunk.hip", "calibrate.hip",
-           "kv_cache.hip", "kv_cache8.hip", "kv_attend.hip", "residual_norm.hip"]
+           "kv_cache.hip", "kv_cache8.hip", "kv_attend.hip", "kv_attend_shared.hip", "residual_norm.hip"]
 ARCH = "gfx950"
 
 COMMON = [

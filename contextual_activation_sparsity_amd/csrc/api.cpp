@@ -621,7 +621,6 @@ void set_plan(sfn::AttendArgs& a, const sfn::AttendPlan& p, const sfn_kv* kv, ch
   a.row_tiles = p.row_tiles;
   a.S = p.S;
   a.chunk = p.chunk;
-  a.groups = p.groups;
 }
 
 int attend(const sfn_kv* kv, const uint8_t* k_exp, const uint8_t* v_exp, int32_t R, int32_t T, int32_t h_q, const void* q, int64_t q_stride,
@@ -689,34 +688,31 @@ int attend_shared(const sfn_kv* kv, const uint8_t* k_exp, const uint8_t* v_exp, 
   if (!aligned16(out)) return SFN_EALIGN;
   for (const int32_t* p : {prefix, shared_len, table, cu, kv_len})
     if (!aligned4_or_null(p)) return SFN_EALIGN;
+  max_new = std::min(max_new, T);
   const sfn::AttendPlan po = sfn::attend_plan(R, h_q, kv->h_kv, kv->dtype, max_new, own_span(max_own), 0);
   const sfn::AttendPlan pp = sfn::prefix_plan(T, h_q, kv->h_kv, kv->dtype, max_shared);
-  if ((int64_t)R * po.S * po.row_tiles * kv->h_kv > INT32_MAX || (int64_t)pp.S * pp.row_tiles * kv->h_kv > INT32_MAX) return SFN_ESHAPE;
+  if ((int64_t)R * (po.S | 1) * po.row_tiles * kv->h_kv + (int64_t)pp.S * pp.row_tiles * kv->h_kv > INT32_MAX) return SFN_ESHAPE;
   const int64_t own_parts = shared_parts((int64_t)R * max_new * h_q, po), prefix_parts = shared_parts((int64_t)T * h_q, pp);
   if ((st = check_ws(ws, ws_bytes, shared_bytes(kv, own_parts, prefix_parts))) != SFN_OK) return st;
   char* const w = static_cast<char*>(ws) + sfn::kWsHeader;
-  sfn::AttendArgs a = attend_args(kv, k_exp, v_exp, T, h_q, q, q_stride, cu, kv_len, scale, out);
-  a.shared = shared_len;
-  a.max_shared = max_shared;
-  a.max_own = max_own;
-  sfn::AttendArgs b = a;
-  set_plan(a, po, kv, w, own_parts);
-  a.kind = sfn::ATTEND_OWN;
-  a.cu_step = 1;
-  a.table = table;
-  a.max_pages = max_pages;
-  a.R = R;
-  a.max_new = max_new;
-  a.max_len = (int32_t)std::min<int64_t>((int64_t)max_pages * kv->page, max_shared + max_own);
-  set_plan(b, pp, kv, w + (attend_bytes(kv, own_parts) - sfn::kWsHeader), prefix_parts);
-  b.kind = sfn::ATTEND_PREFIX;
-  b.cu_step = R;
-  b.table = prefix;
-  b.max_pages = prefix_pages;
-  b.R = 1;
-  b.max_new = T;
-  b.max_len = max_shared;
-  return hip_status(sfn::launch_kv_attend_shared(a, b, kv->dh, kv->dtype, static_cast<hipStream_t>(stream)));
+  sfn::SharedArgs a{};
+  a.own = attend_args(kv, k_exp, v_exp, T, h_q, q, q_stride, cu, kv_len, scale, out);
+  a.own.R = R;
+  a.own.shared = shared_len;
+  a.own.max_shared = max_shared;
+  a.own.max_own = max_own;
+  a.prefix = a.own;
+  set_plan(a.own, po, kv, w, own_parts);
+  a.own.table = table;
+  a.own.max_pages = max_pages;
+  a.own.max_new = max_new;
+  a.own.max_len = (int32_t)std::min<int64_t>((int64_t)max_pages * kv->page, max_shared + max_own);
+  set_plan(a.prefix, pp, kv, w + (attend_bytes(kv, own_parts) - sfn::kWsHeader), prefix_parts);
+  a.prefix.table = prefix;
+  a.prefix.max_pages = prefix_pages;
+  a.prefix.max_new = T;
+  a.prefix.max_len = max_shared;
+  return hip_status(sfn::launch_kv_attend_shared(a, kv->dh, kv->dtype, static_cast<hipStream_t>(stream)));
 }
 
 }  // namespace

@@ -135,9 +135,6 @@ struct Kv8ReadArgs {
 };
 hipError_t launch_kv8_read(const Kv8ReadArgs& a, int dh, int dtype, hipStream_t stream);
 
-// What a launch of a call over a shared prefix attends to: the prefix, of all tokens as one
-// request, or each request's keys behind it.
-enum { ATTEND_PREFIX = 0, ATTEND_OWN = 1 };
 struct AttendArgs {
   const char *k, *v, *q;
   int64_t q_stride;  // bytes from token to token
@@ -145,17 +142,16 @@ struct AttendArgs {
   char* out;
   float *part_o, *part_ml;  // [R, max_new, h_q, S, dh] and [R, max_new, h_q, S, 2] (S > 1)
   int R, T, h_q, h_kv, g, g_mul, page_shift, n_pages, max_pages, max_new, max_len, window;
-  int tile_rows, tile_keys, row_tiles, S, chunk, groups;  // see AttendPlan
+  int tile_rows, tile_keys, row_tiles, S, chunk;  // see AttendPlan
   float scale_log2;                               // score scale times log2(e)
   const uint8_t *k_exp, *v_exp;                   // the rows' powers of two of an 8-bit cache, else null
-  const int32_t* shared;                          // from here on, of a call over a shared prefix
-  int kind, cu_step, max_shared, max_own;         // request r's tokens are [cu[r], cu[r + cu_step])
+  const int32_t* shared;                          // tokens of the prefix, of a call over a shared one
+  int max_shared, max_own;
 };  // g = h_q / h_kv, g_mul = ceil(2^21 / g)
 struct AttendPlan {
   int tile_rows, tile_keys;  // query rows of a workgroup, keys it takes at a time
   int row_tiles, S, chunk;   // workgroups for a key head's rows and for its keys, keys of a split
   int64_t parts;             // rows of partial results
-  int groups;                // tile kernel: groups of four waves
 };
 AttendPlan attend_plan(int R, int h_q, int h_kv, int dtype, int max_new, int max_len, int window);
 // The part of a call over a shared prefix: T tokens as one request over up to max_shared keys.
@@ -164,7 +160,12 @@ int64_t prefix_most_parts(int T, int h_q, int h_kv, int dtype, int max_shared);
 // Rows of partial results that no call within these bounds passes.
 int64_t attend_most_parts(int R, int h_q, int h_kv, int dtype, int max_new, int max_len);
 hipError_t launch_kv_attend(const AttendArgs& a, int dh, int dtype, hipStream_t stream);
-hipError_t launch_kv_attend_shared(const AttendArgs& own, const AttendArgs& prefix, int dh, int dtype, hipStream_t stream);
+// The parts of both: one launch, and one that joins them.
+struct SharedArgs {
+  AttendArgs prefix, own;
+  int prefix_groups;  // workgroups of the prefix's part (set by the launch)
+};
+hipError_t launch_kv_attend_shared(const SharedArgs& a, int dh, int dtype, hipStream_t stream);
 
 struct NormArgs {
   const char *h, *y, *w_post, *w_pre, *gate;
