@@ -915,8 +915,8 @@ struct CodeRows {
   __device__ __forceinline__ void load(const SFN_GLOBAL char* rows, const SFN_GLOBAL uint8_t* exps, int lane) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int row = i * RI + lane / LR;
-      w[i] = ld16(rows + row * DH + (lane % LR) * 16);
+      const uint32_t row = i * RI + lane / LR;  // one address for the wave and an offset for the lane
+      w[i] = ld16(rows + (row * DH + (lane % LR) * 16));
       b[i] = exps[row];
     }
   }
@@ -986,7 +986,7 @@ __device__ __forceinline__ void tile_attention(const AttendArgs& a, uint32_t bx,
 
   const int group = kg * 2 * STAGE, mine = group + 16 * wave * ROW;
   const int kg0 = k0 + kg * KT;
-  CodeRows<DH> kc, vc;
+  CodeRows<DH> kc{}, vc{};
   auto load = [&](char* stage, int64_t row) __attribute__((always_inline)) {
     if constexpr (k8) {
       kc.load(gp(a.k) + row * CROW, gp(a.k_exp) + row, lane);

@@ -78,6 +78,9 @@ __global__ __launch_bounds__(256) void attend_join_shared_kernel(SharedArgs x) {
   const SFN_GLOBAL f32x4_t* o_a = reinterpret_cast<const SFN_GLOBAL f32x4_t*>(gp(a.part_o) + at_a * DH) + d4;
   const SFN_GLOBAL f32x4_t* o_p = reinterpret_cast<const SFN_GLOBAL f32x4_t*>(gp(p.part_o) + at_p * DH) + d4;
   auto part = [&](int s) { return s < mine ? o_a[(int64_t)s * LD] : o_p[(int64_t)(s - mine) * LD]; };
+  f32x4_t v[U];  // the first of them on their way while the weights are found
+#pragma unroll
+  for (int u = 0; u < U; ++u) v[u] = part(min(s0 + u * NS, all - 1));
 
   float m[NK], l[NK], M = kNegInf;
 #pragma unroll
@@ -112,12 +115,13 @@ __global__ __launch_bounds__(256) void attend_join_shared_kernel(SharedArgs x) {
   }
   f32x4_t o = {0.f, 0.f, 0.f, 0.f};
   for (int s = s0; s < all; s += U * NS) {
-    f32x4_t v[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) v[u] = part(min(s + u * NS, all - 1));
 #pragma unroll
     for (int u = 0; u < U; ++u)
       if (s + u * NS < all) o += v[u] * w_of[s + u * NS];  // also for weight 0: NaN scores show
+    if (s + U * NS < all) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) v[u] = part(min(s + (U + u) * NS, all - 1));
+    }
   }
   f32x4_t* const o_of = s_o + (WAVE ? 64 * wave : 0);
   o_of[tid] = o;
@@ -158,11 +162,15 @@ void launch_shared(SharedArgs a, hipStream_t stream) {
 
 }  // namespace
 
-#ifndef T_ROUNDS
-#define T_ROUNDS 8
-#define T_PARTS 6500
-#endif
-constexpr int kSlots = 512, kHalfRounds = 2 * T_ROUNDS, kPartsOfStage = T_PARTS;
+// The prefix's keys are the same for all its row tiles, so that their splits can be chosen to fill
+// the chip evenly: of numbers of workgroups up to kHalfRounds quarters of a round (two to a compute
+// unit) the one with the lowest cost, which is the stages of the longest chain of rounds, each as
+// long as writing and joining kPartsOfStage rows of parts. 32 chunks of up to 16 tokens after
+// 60000 shared keys, 64 / 8 heads, in 8 bits: 641 us, unsplit (152 workgroups) 1186.
+// kPartsOfStage 3000, with 6500 in brackets, bf16, 32 / 8 heads: 48 single tokens after 8000 shared
+// keys 42.9 us (45.9), 64 after 30000 66.1 (68.9), 4 chunks of 16 after 8000, 64 / 8 heads, 35.4
+// (41.4), 4 prompts of 150 after 4000 47.4 (55.1); with 1500 48 after 8000 in 8 bits 41.3 (37.7).
+constexpr int kSlots = 512, kHalfRounds = 16, kPartsOfStage = 3000;
 AttendPlan prefix_plan(int T, int h_q, int h_kv, int dtype, int max_shared) {
   AttendPlan p = attend_plan(1, h_q, h_kv, dtype, T, max_shared, 0);
   if (p.tile_rows != kTileRows) return p;
