@@ -132,6 +132,7 @@ struct Kv8ReadArgs {
   char *k_out, *v_out;
   int64_t k_stride, v_stride;  // bytes from token to token
   int T, h_kv, n_pages, page_shift;
+  int tokens;  // of a workgroup (set by the launch)
 };
 hipError_t launch_kv8_read(const Kv8ReadArgs& a, int dh, int dtype, hipStream_t stream);
 

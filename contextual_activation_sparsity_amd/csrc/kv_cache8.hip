@@ -24,6 +24,9 @@ namespace {
 // bits, whatever the order of operations; in 32 bits one value in a million would fall on the
 // other side of a border between two codes. On the way to 32 bits the value is rounded to odd
 // (cut, its last bit set if anything was lost), which a second rounding does not notice.
+// Bound by memory: 8000 tokens, 64 / 8 heads of 128, 316 MB in 66.6 us, 4.7 TB/s where a large copy
+// reaches 5.1; the 64-bit products take no time beside it. Past-the-caches reads 69 us, the cache's
+// rows before the queries 69.5, 512 threads 72. Four tokens 3.5 us, latency.
 template <int WT>
 struct Eight;  // 8 values of a row
 template <>
@@ -91,38 +94,40 @@ __global__ __launch_bounds__(256) void kv8_append_kernel(Kv8AppendArgs a) {
   if (half) rope = gp(a.rope) + (int64_t)min(max(gp(a.pos)[t], 0), a.n_pos - 1) * a.rot;
 
   // queries
-  const SFN_GLOBAL char* q = gp(a.q) + (int64_t)t * a.q_stride;
-  SFN_GLOBAL char* qo = gp(a.q_out) + (int64_t)t * a.h_q * DH * kB;
-  const int units = half / 8;
-  if (units && a.h_q) {
-    const int u = tid % units, step = nt / units;
-    float c[8], s[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      c[i] = rope[u * 8 + i];
-      s[i] = rope[half + u * 8 + i];
-    }
-    for (int h = tid / units; h < a.h_q && tid < units * step; h += step) {
-      float x[8], y[8], xr[8], yr[8];
-      Eight<WT>::load(q + h * DH * kB, u * 8, x);
-      Eight<WT>::load(q + h * DH * kB, half + u * 8, y);
+  if (blockIdx.y == 0) {
+    const SFN_GLOBAL char* q = gp(a.q) + (int64_t)t * a.q_stride;
+    SFN_GLOBAL char* qo = gp(a.q_out) + (int64_t)t * a.h_q * DH * kB;
+    const int units = half / 8;
+    if (units && a.h_q) {
+      const int u = tid % units, step = nt / units;
+      float c[8], s[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        xr[i] = x[i] * c[i] - y[i] * s[i];
-        yr[i] = y[i] * c[i] + x[i] * s[i];
+        c[i] = rope[u * 8 + i];
+        s[i] = rope[half + u * 8 + i];
       }
-      Eight<WT>::store(qo + h * DH * kB, u * 8, xr);
-      Eight<WT>::store(qo + h * DH * kB, half + u * 8, yr);
+      for (int h = tid / units; h < a.h_q && tid < units * step; h += step) {
+        float x[8], y[8], xr[8], yr[8];
+        Eight<WT>::load(q + h * DH * kB, u * 8, x);
+        Eight<WT>::load(q + h * DH * kB, half + u * 8, y);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          xr[i] = x[i] * c[i] - y[i] * s[i];
+          yr[i] = y[i] * c[i] + x[i] * s[i];
+        }
+        Eight<WT>::store(qo + h * DH * kB, u * 8, xr);
+        Eight<WT>::store(qo + h * DH * kB, half + u * 8, yr);
+      }
+    }
+    const int rest = (DH - a.rot) / 8;  // eights of a head that are not turned
+    for (int i = tid; i < a.h_q * rest; i += nt) {
+      const int h = i / rest, at = a.rot + (i % rest) * 8;
+      float x[8];
+      Eight<WT>::load(q + h * DH * kB, at, x);
+      Eight<WT>::store(qo + h * DH * kB, at, x);
     }
   }
-  const int rest = (DH - a.rot) / 8;  // eights of a head that are not turned
-  for (int i = tid; i < a.h_q * rest; i += nt) {
-    const int h = i / rest, at = a.rot + (i % rest) * 8;
-    float x[8];
-    Eight<WT>::load(q + h * DH * kB, at, x);
-    Eight<WT>::store(qo + h * DH * kB, at, x);
-  }
-  if (!put) return;
+  if (!put || (gridDim.y == 2 && blockIdx.y == 0)) return;
 
   // keys, then values; whole waves take part in the maxima
   const int64_t cell = (((int64_t)(slot >> lg) * a.h_kv) << lg) + (slot & ((1 << lg) - 1));  // head 0's row in the cache
@@ -168,41 +173,72 @@ __global__ __launch_bounds__(256) void kv8_append_kernel(Kv8AppendArgs a) {
 // ---- read ----------------------------------------------------------------------------
 //
 // Rows of K and V by slots, as the values they stand for: exact in bf16 and fp32 (four bits of
-// significand and a power of two). A lane turns 8 codes; a token is one workgroup's.
-template <int WT, int DH>
+// significand and a power of two). Bound by memory: 60000 tokens, 8 heads of 128, 370 MB in 70 us,
+// 5.3 TB/s, in bf16; 20000 in fp32, 205 MB in 40.5 us. A lane turns 16 codes into bf16 (with 8: 79
+// us), 8 into fp32 (with 16 its stores lie too far apart: 122 us), and a workgroup takes as many
+// tokens as give all of its lanes a piece (60000 tokens of 2 heads of 64, one token to a workgroup
+// 16 us, with eight 10.9). Codes are read once and past the caches; results that the caches would
+// not hold go past them too (70 instead of 77 us), others do not (2000 tokens 3.7 instead of 4.2).
+template <int WT>
+constexpr int kReadCodes = WT == WT_BF16 ? 16 : 8;
+
+template <int WT, int DH, bool PAST>
 __global__ __launch_bounds__(256) void kv8_read_kernel(Kv8ReadArgs a) {
-  constexpr int kB = WT == WT_BF16 ? 2 : 4, L = DH / 8;
-  const int t = blockIdx.x, lg = a.page_shift;
-  const int slot = gp(a.slot)[t];
-  const bool held = slot >= 0 && (slot >> lg) < a.n_pages;
-  const int64_t cell = held ? (((int64_t)(slot >> lg) * a.h_kv) << lg) + (slot & ((1 << lg) - 1)) : 0;
-  for (int i = threadIdx.x; i < 2 * a.h_kv * L; i += blockDim.x) {
-    const int r = i / L, j8 = (i % L) * 8;
-    const bool key = r < a.h_kv;
+  constexpr int kB = WT == WT_BF16 ? 2 : 4, E = kReadCodes<WT>, L = DH / E;
+  const int lg = a.page_shift, per = 2 * a.h_kv * L;  // lanes of a token
+  for (int i = threadIdx.x; i < a.tokens * per; i += blockDim.x) {
+    const int t = blockIdx.x * a.tokens + i / per, r = i % per / L, at = (i % L) * E;
+    if (t >= a.T) return;
+    const int slot = gp(a.slot)[t];
+    const bool held = slot >= 0 && (slot >> lg) < a.n_pages, key = r < a.h_kv;
     const int h = key ? r : r - a.h_kv;
-    const int64_t from = cell + ((int64_t)h << lg);
-    float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    float x[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) x[e] = 0.f;
     if (held) {
-      const uint64_t w = *reinterpret_cast<const SFN_GLOBAL uint64_t*>((key ? gp(a.k_cache) : gp(a.v_cache)) + from * DH + j8);
+      const int64_t from = ((((int64_t)(slot >> lg) * a.h_kv) + h) << lg) + (slot & ((1 << lg) - 1));
+      const SFN_GLOBAL char* p = (key ? gp(a.k_cache) : gp(a.v_cache)) + from * DH + at;
       const float scale = scale_of((key ? gp(a.k_exp) : gp(a.v_exp))[from]);
-      values_of((uint32_t)w, scale, x);
-      values_of((uint32_t)(w >> 32), scale, x + 4);
+      typedef __attribute__((ext_vector_type(E / 4))) uint32_t Codes;
+      const Codes w = __builtin_nontemporal_load(reinterpret_cast<const SFN_GLOBAL Codes*>(p));
+#pragma unroll
+      for (int e = 0; e < E; e += 4) values_of(w[e / 4], scale, x + e);
     }
-    Eight<WT>::store((key ? gp(a.k_out) + (int64_t)t * a.k_stride : gp(a.v_out) + (int64_t)t * a.v_stride) + h * DH * kB, j8, x);
+    SFN_GLOBAL char* to = (key ? gp(a.k_out) + (int64_t)t * a.k_stride : gp(a.v_out) + (int64_t)t * a.v_stride) + (h * DH + at) * kB;
+#pragma unroll
+    for (int e = 0; e < E; e += 16 / kB) {
+      u32x4_t v;
+      if constexpr (WT == WT_BF16)
+        v = u32x4_t{pack_bf16(x[e], x[e + 1]), pack_bf16(x[e + 2], x[e + 3]), pack_bf16(x[e + 4], x[e + 5]), pack_bf16(x[e + 6], x[e + 7])};
+      else
+        v = __builtin_bit_cast(u32x4_t, (f32x4_t{x[e], x[e + 1], x[e + 2], x[e + 3]}));
+      SFN_GLOBAL u32x4_t* const o = reinterpret_cast<SFN_GLOBAL u32x4_t*>(to + e * kB);
+      if constexpr (PAST) __builtin_nontemporal_store(v, o);
+      else *o = v;
+    }
   }
 }
+
+// Up to so many tokens, a token's queries and its rows of the cache are a workgroup each, which run
+// side by side (4 tokens, 32 / 8 heads, 4.00 -> 3.54 us); more fill the chip as they are (8000
+// tokens, 64 / 8 heads, 66.6 us against 78.3, 2000 35.0 both ways).
+constexpr int kApart = 1024;
+constexpr int64_t kHeld = 64 << 20;  // bytes that are written past the caches if there are more
 
 int threads_for(int items) { return items <= 64 ? 64 : items <= 128 ? 128 : 256; }
 
 template <int WT>
 void launch_append(const Kv8AppendArgs& a, int dh, int threads, hipStream_t stream) {
-  if (dh == 64) hipLaunchKernelGGL((kv8_append_kernel<WT, 64>), dim3(a.T), dim3(threads), 0, stream, a);
-  else hipLaunchKernelGGL((kv8_append_kernel<WT, 128>), dim3(a.T), dim3(threads), 0, stream, a);
+  if (dh == 64) hipLaunchKernelGGL((kv8_append_kernel<WT, 64>), dim3(a.T, a.T <= kApart ? 2 : 1), dim3(threads), 0, stream, a);
+  else hipLaunchKernelGGL((kv8_append_kernel<WT, 128>), dim3(a.T, a.T <= kApart ? 2 : 1), dim3(threads), 0, stream, a);
 }
-template <int WT>
-void launch_read(const Kv8ReadArgs& a, int dh, int threads, hipStream_t stream) {
-  if (dh == 64) hipLaunchKernelGGL((kv8_read_kernel<WT, 64>), dim3(a.T), dim3(threads), 0, stream, a);
-  else hipLaunchKernelGGL((kv8_read_kernel<WT, 128>), dim3(a.T), dim3(threads), 0, stream, a);
+template <int WT, int DH>
+void launch_read(Kv8ReadArgs a, hipStream_t stream) {
+  const int per = 2 * a.h_kv * DH / kReadCodes<WT>;
+  a.tokens = std::clamp(256 / per, 1, 16);
+  const dim3 grid((a.T + a.tokens - 1) / a.tokens), threads(threads_for(a.tokens * per));
+  if ((int64_t)a.T * a.h_kv * DH * (WT == WT_BF16 ? 4 : 8) > kHeld) hipLaunchKernelGGL((kv8_read_kernel<WT, DH, true>), grid, threads, 0, stream, a);
+  else hipLaunchKernelGGL((kv8_read_kernel<WT, DH, false>), grid, threads, 0, stream, a);
 }
 
 }  // namespace
@@ -215,9 +251,13 @@ hipError_t launch_kv8_append(const Kv8AppendArgs& a, int dh, int dtype, hipStrea
 }
 
 hipError_t launch_kv8_read(const Kv8ReadArgs& a, int dh, int dtype, hipStream_t stream) {
-  const int threads = threads_for(2 * a.h_kv * dh / 8);
-  if (dtype == SFN_BF16) launch_read<WT_BF16>(a, dh, threads, stream);
-  else launch_read<WT_F32>(a, dh, threads, stream);
+  if (dtype == SFN_BF16) {
+    if (dh == 64) launch_read<WT_BF16, 64>(a, stream);
+    else launch_read<WT_BF16, 128>(a, stream);
+  } else {
+    if (dh == 64) launch_read<WT_F32, 64>(a, stream);
+    else launch_read<WT_F32, 128>(a, stream);
+  }
   return hipGetLastError();
 }
 
