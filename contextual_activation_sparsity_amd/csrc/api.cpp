@@ -691,7 +691,8 @@ int attend_shared(const sfn_kv* kv, const uint8_t* k_exp, const uint8_t* v_exp, 
   max_new = std::min(max_new, T);
   const sfn::AttendPlan po = sfn::attend_plan(R, h_q, kv->h_kv, kv->dtype, max_new, own_span(max_own), 0);
   const sfn::AttendPlan pp = sfn::prefix_plan(T, h_q, kv->h_kv, kv->dtype, max_shared);
-  if ((int64_t)R * (po.S | 1) * po.row_tiles * kv->h_kv + (int64_t)pp.S * pp.row_tiles * kv->h_kv > INT32_MAX) return SFN_ESHAPE;
+  // one launch of 256 threads to a workgroup, whose threads are counted in 32 bits
+  if ((int64_t)R * (po.S | 1) * po.row_tiles * kv->h_kv + (int64_t)pp.S * pp.row_tiles * kv->h_kv > UINT32_MAX / 256) return SFN_ESHAPE;
   const int64_t own_parts = shared_parts((int64_t)R * max_new * h_q, po), prefix_parts = shared_parts((int64_t)T * h_q, pp);
   if ((st = check_ws(ws, ws_bytes, shared_bytes(kv, own_parts, prefix_parts))) != SFN_OK) return st;
   char* const w = static_cast<char*>(ws) + sfn::kWsHeader;

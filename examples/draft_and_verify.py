@@ -1,7 +1,7 @@
 #!/usr/bin/env python3
 """A small decoder served with the library: sparse drafts, dense verification, rollback.
 
-    python examples/draft_and_verify.py [--requests 3] [--tokens 48] [--draft 16]
+    python examples/draft_and_verify.py [--requests 3] [--tokens 48] [--draft 16] [--cache own|e4m3]
 
 Several requests are decoded greedily at once ("SIRIUS: Contexual Sparisty with Correction
 for Efficient LLMs", Approach). Each period drafts up to 16 tokens a request with the sparse
@@ -10,9 +10,9 @@ chunk through the full layers (``ffn_dense_chunk``), keeps the tokens on which b
 one of the full model's own, and drops the rest. The paged cache carries this: the plan takes
 pages for new tokens and gives back those of dropped ones, ``kv_cache_append`` rewrites the
 drafted positions with the full model's keys and values, ``kv_cache_attend`` serves single
-tokens, chunks and prompts alike, and ``residual_norm`` stands between all blocks. Weights are
-random (so the agreement means nothing beyond showing the mechanism); the projections are
-plain torch products.
+tokens, chunks and prompts alike, and ``residual_norm`` stands between all blocks; with ``--cache e4m3``
+the cache holds 8 bits a value (the ``kv8_cache`` calls). Weights are random (so the agreement
+means nothing beyond showing the mechanism); the projections are plain torch products.
 """
 
 import argparse
@@ -29,7 +29,7 @@ class Decoder:
     """Layers, their caches, and the bookkeeping of one batch of requests."""
 
     def __init__(self, layers=2, d=256, f=688, h_q=4, h_kv=2, dh=64, vocab=500, requests=3, max_len=256, page=16,
-                 sparsity=0.5, dtype=torch.float32, seed=0):
+                 sparsity=0.5, dtype=torch.float32, seed=0, cache="own"):
         g = torch.Generator(device="cuda")
         g.manual_seed(seed)
         rnd = lambda *s, std: (torch.randn(s, generator=g, device="cuda") * std).to(dtype)  # noqa: E731
@@ -39,18 +39,25 @@ class Decoder:
         cols = -(-max_len // page)
         n_pages = requests * cols
         for _ in range(layers):
-            cache = B.KVCache(*(torch.zeros((n_pages, h_kv, page, dh), dtype=dtype, device="cuda") for _ in range(2)))
+            if cache == "e4m3":
+                k, v = (torch.zeros((n_pages, h_kv, page, dh), dtype=torch.float8_e4m3fn, device="cuda") for _ in range(2))
+                kv = B.KVCache8(k, v, *(torch.zeros((n_pages, h_kv, page), dtype=torch.uint8, device="cuda") for _ in range(2)), dtype)
+            else:
+                kv = B.KVCache(*(torch.zeros((n_pages, h_kv, page, dh), dtype=dtype, device="cuda") for _ in range(2)))
             ffn = B.FFNLayer(rnd(f, d, std=d ** -0.5), rnd(f, d, std=d ** -0.5), rnd(f, d, std=f ** -0.5))
             self.layers.append(dict(
-                qkv=rnd(h_q * dh + 2 * h_kv * dh, d, std=d ** -0.5), out=rnd(d, h_q * dh, std=(h_q * dh) ** -0.5), ffn=ffn, cache=cache,
+                qkv=rnd(h_q * dh + 2 * h_kv * dh, d, std=d ** -0.5), out=rnd(d, h_q * dh, std=(h_q * dh) ** -0.5), ffn=ffn, cache=kv,
                 before_ffn=B.ResidualNorm(1 + rnd(d, std=0.1)), after_ffn=B.ResidualNorm(1 + rnd(d, std=0.1)),
                 threshold=torch.empty(1, device="cuda")))
         self.first = B.ResidualNorm(1 + rnd(d, std=0.1))
         ang = torch.arange(max_len, device="cuda")[:, None] * 10000.0 ** (-torch.arange(0, dh, 2, device="cuda") / dh)[None]
         self.rope = torch.cat([ang.cos(), ang.sin()], 1).float().contiguous()
+        self.append, self.attend, attend_size = (
+            (B.kv8_cache_append, B.kv8_cache_attend, B.kv8_cache_attend_workspace_size) if cache == "e4m3" else
+            (B.kv_cache_append, B.kv_cache_attend, B.kv_cache_attend_workspace_size))
         # one workspace serves every call: they run in order on one stream
         ffn = self.layers[0]["ffn"]
-        self.ws = B.workspace(max(B.sparse_ffn_workspace_size(ffn, 256), B.kv_cache_attend_workspace_size(
+        self.ws = B.workspace(max(B.sparse_ffn_workspace_size(ffn, 256), attend_size(
             self.layers[0]["cache"], requests, requests * max_len, h_q, max_len, max_len)))
         x = rnd(256, d, std=1.0)
         for layer in self.layers:  # the sparse FFN's thresholds, from tokens of the norm's scale
@@ -80,9 +87,9 @@ class Decoder:
         B.residual_norm(self.first, h, None, None, x)
         for layer in self.layers:
             qkv = (x @ layer["qkv"].t()).view(T, self.h_q + 2 * self.h_kv, self.dh)
-            B.kv_cache_append(layer["cache"], qkv[:, self.h_q:-self.h_kv], qkv[:, -self.h_kv:], slot, q=qkv[:, :self.h_q],
-                              q_out=q, pos=pos, rope=self.rope)
-            B.kv_cache_attend(layer["cache"], q, self.table, self.cu, self.kv_len, a, self.ws, max(max(new), 1), self.max_len)
+            self.append(layer["cache"], qkv[:, self.h_q:-self.h_kv], qkv[:, -self.h_kv:], slot, q=qkv[:, :self.h_q],
+                        q_out=q, pos=pos, rope=self.rope)
+            self.attend(layer["cache"], q, self.table, self.cu, self.kv_len, a, self.ws, max(max(new), 1), self.max_len)
             B.residual_norm(layer["before_ffn"], h, a.view(T, -1) @ layer["out"].t(), h, x)
             at = B.SFN_MAX_CHUNK if dense else B.SFN_MAX_BATCH
             for i in range(0, T, at):
@@ -131,8 +138,9 @@ def main(argv=None):
     ap.add_argument("--requests", type=int, default=3, choices=range(1, B.SFN_MAX_BATCH + 1))
     ap.add_argument("--tokens", type=int, default=48)
     ap.add_argument("--draft", type=int, default=16)
+    ap.add_argument("--cache", choices=("own", "e4m3"), default="own")
     a = ap.parse_args(argv)
-    model = Decoder(requests=a.requests, dtype=torch.bfloat16, max_len=64 + a.tokens + 16)
+    model = Decoder(requests=a.requests, dtype=torch.bfloat16, max_len=64 + a.tokens + 16, cache=a.cache)
     prompts = [[(7 * r + 3 * i) % 500 for i in range(5 + 11 * r)] for r in range(a.requests)]
     seqs, kept, drafted = model.generate(prompts, a.tokens, a.draft)
     print(f"{a.requests} requests, {a.tokens} tokens each: {kept} of {drafted} drafted tokens kept; "

@@ -412,7 +412,8 @@ int kv_cache_attend(const sfn_kv* kv, int32_t R, int32_t T, int32_t h_q, const v
  *            *shared_len counts as max_shared (or the tokens of prefix_pages) at most, a kv_len as
  *            *shared_len + max_own at most, or as max_own where the request reads its own row alone
  * Requests with other prefixes are calls of their own (with rows of table, cu and kv_len, as
- * above). Workspace: as kv_cache_attend's, enough for every call with smaller arguments.
+ * above), and so are prompts beside single tokens: R times the row tiles of max_new tokens are
+ * launched, and more than 2^24 of them, over all heads and splits, are refused. Workspace: as kv_cache_attend's, enough for every call with smaller arguments.
  * T = 0 does nothing.
  */
 size_t kv_cache_attend_shared_workspace_size(const sfn_kv* kv, int32_t R, int32_t T, int32_t h_q, int32_t max_new,
@@ -453,7 +454,8 @@ int kv8_cache_append(const sfn_kv8* kv, int32_t T, int32_t h_q, const void* q, i
 
 /*
  * Reads tokens' keys and values back, by slots (as kv_cache_append takes them; any order, a slot
- * as often as wanted): to keep a request's tokens elsewhere, or to append them to another cache.
+ * as often as wanted): to keep a request's tokens elsewhere, or to append them to another cache
+ * (with the same rows of codes, if nothing is rotated again). T <= 262144.
  *   slot     [T]; a slot outside the cache gives zeros
  *   k_out, v_out  token t's heads at k_out + t * k_stride (elements), each head's dh values
  *            contiguous, in kv.dtype, exact; addresses and strides 16-byte aligned

@@ -124,6 +124,14 @@ def test_shared_refusals(kw, status):
     assert shared(**kw) == getattr(B, "SFN_" + status) and shared(_kv(), **kw) == getattr(B, "SFN_" + status)
 
 
+def test_shared_launches_past_32_bits_of_threads_are_refused():
+    """4096 requests whose bound is 4096 tokens of 64 query heads over 8: 8.4 million row tiles over the
+    heads are launched; the same over 32 key heads are too many."""
+    big = dict(R=4096, T=262144, max_new=8192, max_shared=100, max_own=300, ws_bytes=1 << 60, ws=FAKE + 16)
+    assert shared(_kv8(h_kv=8), h_q=32, qs=4096, **big) == B.SFN_EALIGN  # it gets to the workspace
+    assert shared(_kv8(h_kv=32), h_q=128, qs=16384, **big) == B.SFN_ESHAPE
+
+
 def test_no_tokens_is_no_work():
     assert append(T=0, q=None, k=None, v=None, slot=None) == B.SFN_OK and read(T=0, slot=None, k=None, v=None) == B.SFN_OK
     assert attend(T=0, q=None, out=None) == B.SFN_OK and shared(T=0, q=None, out=None) == B.SFN_OK
