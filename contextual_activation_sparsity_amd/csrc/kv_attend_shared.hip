@@ -15,10 +15,18 @@ namespace {
 // (all of them see all of it), each request's other keys by its own rows, and the parts are joined.
 // One launch does both: the first workgroups take row tiles and splits of the prefix, which the
 // products or the latency of its few stages bound, the others the requests' own keys, which
-// memory binds; side by side they take about as long as the longer of them. ATTEND in a name is the
-// way that attend_device.h takes for the rows of one key head: 1 and 2 are split attention with
-// 16 and 32 rows to a workgroup, 3 is tile attention; T tokens have at least as many rows as one
-// request's, so the prefix's way is never the smaller one.
+// memory binds; side by side they take about as long as the longer of them. As two launches (a
+// prefix's and the requests', then the join) 6 fp32 chunks over 300 shared keys took 14.1 us where
+// this takes 9.3, 8 tokens after 2000 shared keys 19.7 (13.2), 48 after 8000 48.2 (46.0), 32 chunks
+// after 60000 665 (641).
+// WAY is how a workgroup takes the rows of one key head: 1 and 2 are split attention with 16 and 32
+// rows, 3 is tile attention. T tokens have at least as many rows as one request's, so the prefix's
+// way is never the smaller one. The registers of a launch are those of its larger way: with 16 rows
+// in both parts three workgroups share a compute unit, otherwise two.
+// 48 single tokens after 8000 shared keys, each with up to 1200 of its own, 32 / 8 heads of 128,
+// bf16, 123 MB: 42.5 us, 36 in this launch and 6 to 7 in the join, 2.9 TB/s. The requests' part
+// alone takes 22 us with three workgroups to a compute unit and 31 with two; two tiles of keys held
+// at once there (255 registers), or the first page guessed from the shared length, gave 1 to 2%.
 template <int WT, int CT, int DH, int WAY, int KIND, int SIZE_A, int SIZE_B>
 __device__ __forceinline__ void attend_way(const AttendArgs& a, uint32_t bx, int split, int r, char (&s_a)[SIZE_A], char (&s_b)[SIZE_B],
                                            float (&s_m)[4][32], float (&s_l)[4][32]) {
@@ -71,7 +79,8 @@ __global__ __launch_bounds__(256) void attend_join_shared_kernel(SharedArgs x) {
   const int mine = splits_used(a, req, i, head);
   const int all = mine + (req.past >= shared ? (shared + p.chunk - 1) / p.chunk : 0);
   const int64_t at_a = (((int64_t)r * a.max_new + i) * a.h_q + head) * a.S;
-  const int64_t at_p = ((int64_t)(req.t0 + i - first) * a.h_q + head) * p.S;
+  const int token = max(req.t0 + i - first, 0);  // of the prefix's rows; cu that descends stays in them
+  const int64_t at_p = ((int64_t)token * a.h_q + head) * p.S;
   const SFN_GLOBAL f32x2_t* ml_a = reinterpret_cast<const SFN_GLOBAL f32x2_t*>(gp(a.part_ml)) + at_a;
   const SFN_GLOBAL f32x2_t* ml_p = reinterpret_cast<const SFN_GLOBAL f32x2_t*>(gp(p.part_ml)) + at_p;
   const int d4 = tid % LD, s0 = tid / LD;

@@ -255,6 +255,20 @@ def test_bounds_that_are_too_small(dtype, kind):
 
 
 @pytest.mark.parametrize("dtype,kind", KINDS)
+@pytest.mark.parametrize("more", [0, 40])
+def test_offsets_that_descend_stay_in_bounds(dtype, kind, more):
+    """The prefix is attended to by the tokens from cu[0] on: those before it, which offsets that
+    descend name, get something from within the parts, the others their own."""
+    shared, n = 700, 2 + more
+    b = Batch(dtype, kind, 2, 64, 16, shared, after(shared, [(20, 0), (30 + n, n), (40 + n, 2 * n)]), 3)
+    b.cu = [2 * n, 0, n, 3 * n]
+    q = tokens(b, 8, 64, 3)
+    out = b.run(q)
+    (_, want, bound), = attend_oracle(q, b.k, b.v, b.table[2:], b.cu[2:], b.lens[2:], 0, 64 ** -0.5)
+    within(out[2 * n:], want[n:], bound[n:], "the tokens behind cu[0]")
+
+
+@pytest.mark.parametrize("dtype,kind", KINDS)
 def test_prefix_pages_out_of_range_stay_in_the_cache(dtype, kind):
     b = Batch(dtype, kind, 2, 64, 16, 64, after(64, [(20, 1), (9, 1)]), 17)
     if kind == "e4m3":
