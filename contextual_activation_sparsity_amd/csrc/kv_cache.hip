@@ -164,37 +164,6 @@ __global__ __launch_bounds__(kPlanThreads) void kv_plan_kernel(KvPlanArgs a) {
 // copy reaches 5.1; four tokens 2.8 us, latency. Non-temporal stores take 58 us instead of 63
 // alone, but the attention that follows reads what is written here.
 template <int WT>
-struct Row16;
-template <>
-struct Row16<WT_BF16> {
-  static constexpr int kVals = 8;
-  __device__ __forceinline__ static void widen(const uint4& v, float* f) {
-    const uint32_t p[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[2 * i] = __uint_as_float(p[i] << 16);
-      f[2 * i + 1] = __uint_as_float(p[i] & 0xffff0000u);
-    }
-  }
-  __device__ __forceinline__ static uint4 narrow(const float* f) {
-    return make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
-  }
-};
-template <>
-struct Row16<WT_F32> {
-  static constexpr int kVals = 4;
-  __device__ __forceinline__ static void widen(const uint4& v, float* f) {
-    f[0] = __uint_as_float(v.x);
-    f[1] = __uint_as_float(v.y);
-    f[2] = __uint_as_float(v.z);
-    f[3] = __uint_as_float(v.w);
-  }
-  __device__ __forceinline__ static uint4 narrow(const float* f) {
-    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
-  }
-};
-
-template <int WT>
 __global__ __launch_bounds__(256) void kv_append_kernel(KvAppendArgs a) {
   constexpr int E = Row16<WT>::kVals;
   constexpr int kB = WT == WT_BF16 ? 2 : 4;

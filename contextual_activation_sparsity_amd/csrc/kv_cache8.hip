@@ -14,53 +14,37 @@ namespace {
 
 // ---- append --------------------------------------------------------------------------
 //
-// One workgroup per token. Queries are turned as kv_append_kernel turns them: a thread keeps
-// one 8-value unit's cosines and sines and walks the heads with them. A row of K or V (one
-// head's dh values) belongs to dh / 8 neighbouring lanes with 8 values each: the row's largest
-// magnitude is a maximum over those lanes, its power of two a shift of that maximum's bits, and
-// each value is rounded once, by the hardware's conversion to e4m3.
+// One workgroup per token (of a few tokens, two). Queries are turned as kv_append_kernel turns them:
+// a thread keeps the cosines and sines of 16 bytes of values and walks the heads with them. A row of
+// K or V (one head's dh values) belongs to dh / 8 neighbouring lanes: the row's largest magnitude is
+// a maximum over those lanes, its power of two a shift of that maximum's bits, and each value is
+// rounded once, by the hardware's conversion to e4m3. A lane has four values and the four that they
+// are turned with, so that nothing is loaded twice and their cosines and sines are read once for all
+// of the lane's rows (against eight neighbouring values, with the partners and the cosines read for
+// each row: 2000 tokens of 32 / 32 heads 35.2 -> 20.7 us, 6000 of 16 / 16 55.6 -> 36.5).
 // Keys are turned in 64 bits: both products of a bf16 or fp32 value and an fp32 cosine are
 // exact there, so a code is the one nearest to the rotated value but for one rounding to 53
 // bits, whatever the order of operations; in 32 bits one value in a million would fall on the
 // other side of a border between two codes. On the way to 32 bits the value is rounded to odd
 // (cut, its last bit set if anything was lost), which a second rounding does not notice.
-// Bound by memory: 8000 tokens, 64 / 8 heads of 128, 316 MB in 66.6 us, 4.7 TB/s where a large copy
-// reaches 5.1; the 64-bit products take no time beside it. Past-the-caches reads 69 us, the cache's
-// rows before the queries 69.5, 512 threads 72. Four tokens 3.5 us, latency.
+// Bound by memory: 8000 tokens, 64 / 8 heads of 128, 316 MB in 67 us, 4.7 TB/s where a large copy
+// reaches 5.1; with the products in 32 bits it would be 62. Past-the-caches reads, the cache's
+// rows before the queries and 512 threads gave 3 to 8% more time there. Where keys and values
+// are most of it, each wave waits for its rows: 6000 tokens of 16 / 16 heads, 123 MB, 3.4 TB/s.
+// Four tokens 3.0 us, latency.
+// Four values of a row.
 template <int WT>
-struct Eight;  // 8 values of a row
-template <>
-struct Eight<WT_BF16> {
-  __device__ __forceinline__ static void load(const SFN_GLOBAL char* row, int at, float* f) {
-    const uint4 v = ld16(row + at * 2);
-    const uint32_t p[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[2 * i] = __uint_as_float(p[i] << 16);
-      f[2 * i + 1] = __uint_as_float(p[i] & 0xffff0000u);
-    }
+__device__ __forceinline__ void load4(const SFN_GLOBAL char* p, float* f) {
+  if constexpr (WT == WT_BF16) {
+    const uint64_t v = *reinterpret_cast<const SFN_GLOBAL uint64_t*>(p);
+    f[0] = __uint_as_float((uint32_t)v << 16);
+    f[1] = __uint_as_float((uint32_t)v & 0xffff0000u);
+    f[2] = __uint_as_float((uint32_t)(v >> 32) << 16);
+    f[3] = __uint_as_float((uint32_t)(v >> 32) & 0xffff0000u);
+  } else {
+    Row16<WT>::widen(ld16(p), f);
   }
-  __device__ __forceinline__ static void store(SFN_GLOBAL char* row, int at, const float* f) {
-    *reinterpret_cast<SFN_GLOBAL u32x4_t*>(row + at * 2) =
-        u32x4_t{pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7])};
-  }
-};
-template <>
-struct Eight<WT_F32> {
-  __device__ __forceinline__ static void load(const SFN_GLOBAL char* row, int at, float* f) {
-#pragma unroll
-    for (int i = 0; i < 8; i += 4) {
-      const f32x4_t v = *reinterpret_cast<const SFN_GLOBAL f32x4_t*>(row + (at + i) * 4);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) f[i + j] = v[j];
-    }
-  }
-  __device__ __forceinline__ static void store(SFN_GLOBAL char* row, int at, const float* f) {
-#pragma unroll
-    for (int i = 0; i < 8; i += 4)
-      *reinterpret_cast<SFN_GLOBAL f32x4_t*>(row + (at + i) * 4) = f32x4_t{f[i], f[i + 1], f[i + 2], f[i + 3]};
-  }
-};
+}
 
 // d in 32 bits, rounded to odd.
 __device__ __forceinline__ float to_odd(double d) {
@@ -84,7 +68,7 @@ __device__ __forceinline__ bool finite(float x) { return (__float_as_uint(x) & 0
 
 template <int WT, int DH>
 __global__ __launch_bounds__(256) void kv8_append_kernel(Kv8AppendArgs a) {
-  constexpr int kB = WT == WT_BF16 ? 2 : 4, L = DH / 8;  // bytes of a value, lanes of a row
+  constexpr int E = Row16<WT>::kVals, kB = 16 / E, L = DH / 8;  // values of 16 bytes, bytes of one, lanes of a row
   const int t = blockIdx.x, tid = threadIdx.x, nt = blockDim.x;
   const int slot = gp(a.slot)[t];
   const int lg = a.page_shift;
@@ -97,58 +81,73 @@ __global__ __launch_bounds__(256) void kv8_append_kernel(Kv8AppendArgs a) {
   if (blockIdx.y == 0) {
     const SFN_GLOBAL char* q = gp(a.q) + (int64_t)t * a.q_stride;
     SFN_GLOBAL char* qo = gp(a.q_out) + (int64_t)t * a.h_q * DH * kB;
-    const int units = half / 8;
+    auto load = [&](int at, float (&f)[E]) { Row16<WT>::widen(ld16(q + at), f); };
+    auto store = [&](int at, const float (&f)[E]) {
+      const uint4 x = Row16<WT>::narrow(f);
+      *reinterpret_cast<SFN_GLOBAL u32x4_t*>(qo + at) = u32x4_t{x.x, x.y, x.z, x.w};
+    };
+    const int units = half / E;
     if (units && a.h_q) {
       const int u = tid % units, step = nt / units;
-      float c[8], s[8];
+      float c[E], s[E];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        c[i] = rope[u * 8 + i];
-        s[i] = rope[half + u * 8 + i];
+      for (int i = 0; i < E; ++i) {
+        c[i] = rope[u * E + i];
+        s[i] = rope[half + u * E + i];
       }
       for (int h = tid / units; h < a.h_q && tid < units * step; h += step) {
-        float x[8], y[8], xr[8], yr[8];
-        Eight<WT>::load(q + h * DH * kB, u * 8, x);
-        Eight<WT>::load(q + h * DH * kB, half + u * 8, y);
+        const int at = h * DH * kB + u * 16;
+        float x[E], y[E], xr[E], yr[E];
+        load(at, x);
+        load(at + half * kB, y);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < E; ++i) {
           xr[i] = x[i] * c[i] - y[i] * s[i];
           yr[i] = y[i] * c[i] + x[i] * s[i];
         }
-        Eight<WT>::store(qo + h * DH * kB, u * 8, xr);
-        Eight<WT>::store(qo + h * DH * kB, half + u * 8, yr);
+        store(at, xr);
+        store(at + half * kB, yr);
       }
     }
-    const int rest = (DH - a.rot) / 8;  // eights of a head that are not turned
+    const int rest = (DH - a.rot) / E;  // units of a head that are not turned
     for (int i = tid; i < a.h_q * rest; i += nt) {
-      const int h = i / rest, at = a.rot + (i % rest) * 8;
-      float x[8];
-      Eight<WT>::load(q + h * DH * kB, at, x);
-      Eight<WT>::store(qo + h * DH * kB, at, x);
+      const int at = (i / rest * DH + a.rot) * kB + (i % rest) * 16;
+      float x[E];
+      load(at, x);
+      store(at, x);
     }
   }
   if (!put || (gridDim.y == 2 && blockIdx.y == 0)) return;
 
   // keys, then values; whole waves take part in the maxima
   const int64_t cell = (((int64_t)(slot >> lg) * a.h_kv) << lg) + (slot & ((1 << lg) - 1));  // head 0's row in the cache
-  const int rows = 2 * a.h_kv, j8 = (tid % L) * 8;
+  const int rows = 2 * a.h_kv, lane = tid % L;
+  const bool turned = 8 * lane < a.rot;
+  float c[4], s[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    c[i] = turned ? rope[4 * lane + i] : 0.f;
+    s[i] = turned ? rope[half + 4 * lane + i] : 0.f;
+  }
   for (int r0 = 0; r0 < rows; r0 += nt / L) {
     const int r = r0 + tid / L;
     const bool mine = r < rows, key = r < a.h_kv;
     const int h = key ? r : r - a.h_kv;
-    float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    // the lane's values: four from `lo` on, and their partners from `hi` on
+    const int lo = key && !turned ? 8 * lane : 4 * lane, hi = key ? lo + (turned ? half : 4) : lo + DH / 2;
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = 0.f;
     if (mine) {
       const SFN_GLOBAL char* row = (key ? gp(a.k) + (int64_t)t * a.k_stride : gp(a.v) + (int64_t)t * a.v_stride) + h * DH * kB;
-      Eight<WT>::load(row, j8, x);
-      if (key && j8 < a.rot) {
-        const bool low = j8 < half;
-        const int at = low ? j8 : j8 - half;
-        float y[8];
-        Eight<WT>::load(row, low ? j8 + half : at, y);
+      load4<WT>(row + lo * kB, x);
+      load4<WT>(row + hi * kB, x + 4);
+      if (key && turned) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const double sn = low ? -(double)rope[half + at + i] : (double)rope[half + at + i];
-          x[i] = to_odd((double)x[i] * (double)rope[at + i] + (double)y[i] * sn);
+        for (int i = 0; i < 4; ++i) {
+          const double u = x[i], w = x[4 + i], cd = c[i], sd = s[i];
+          x[i] = to_odd(u * cd - w * sd);
+          x[4 + i] = to_odd(w * cd + u * sd);
         }
       }
     }
@@ -163,9 +162,10 @@ __global__ __launch_bounds__(256) void kv8_append_kernel(Kv8AppendArgs a) {
       y[i] = finite(x[i]) ? fminf(fmaxf(x[i] * scale, -448.f), 448.f) : __uint_as_float(0x7fc00000u);
     if (mine) {
       const int64_t to = cell + ((int64_t)h << lg);
-      *reinterpret_cast<SFN_GLOBAL uint64_t*>((key ? gp(a.k_cache) : gp(a.v_cache)) + to * DH + j8) =
-          (uint64_t)pack_e4m3(y[0], y[1], y[2], y[3]) | (uint64_t)pack_e4m3(y[4], y[5], y[6], y[7]) << 32;
-      if (j8 == 0) (key ? gp(a.k_exp) : gp(a.v_exp))[to] = (uint8_t)b;
+      SFN_GLOBAL char* const codes = (key ? gp(a.k_cache) : gp(a.v_cache)) + to * DH;
+      *reinterpret_cast<SFN_GLOBAL uint32_t*>(codes + lo) = pack_e4m3(y[0], y[1], y[2], y[3]);
+      *reinterpret_cast<SFN_GLOBAL uint32_t*>(codes + hi) = pack_e4m3(y[4], y[5], y[6], y[7]);
+      if (lane == 0) (key ? gp(a.k_exp) : gp(a.v_exp))[to] = (uint8_t)b;
     }
   }
 }
@@ -220,8 +220,8 @@ __global__ __launch_bounds__(256) void kv8_read_kernel(Kv8ReadArgs a) {
 }
 
 // Up to so many tokens, a token's queries and its rows of the cache are a workgroup each, which run
-// side by side (4 tokens, 32 / 8 heads, 4.00 -> 3.54 us); more fill the chip as they are (8000
-// tokens, 64 / 8 heads, 66.6 us against 78.3, 2000 35.0 both ways).
+// side by side (4 tokens, 32 / 8 heads, 3.53 us where one after the other took 4.00); more fill the
+// chip as they are (8000 tokens, 64 / 8 heads, 67 us against 73, 2000 of 32 / 32 20.9 against 20.6).
 constexpr int kApart = 1024;
 constexpr int64_t kHeld = 64 << 20;  // bytes that are written past the caches if there are more
 
@@ -244,7 +244,7 @@ void launch_read(Kv8ReadArgs a, hipStream_t stream) {
 }  // namespace
 
 hipError_t launch_kv8_append(const Kv8AppendArgs& a, int dh, int dtype, hipStream_t stream) {
-  const int threads = threads_for(std::max(a.h_q * std::max(a.rot / 2, dh - a.rot) / 8, 2 * a.h_kv * dh / 8));
+  const int e = dtype == SFN_BF16 ? 8 : 4, threads = threads_for(std::max(a.h_q * std::max(a.rot / 2, dh - a.rot) / e, 2 * a.h_kv * dh / 8));
   if (dtype == SFN_BF16) launch_append<WT_BF16>(a, dh, threads, stream);
   else launch_append<WT_F32>(a, dh, threads, stream);
   return hipGetLastError();
