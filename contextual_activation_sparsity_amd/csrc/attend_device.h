@@ -88,6 +88,11 @@ struct Request {
 // fp32 with more rows reads K and V again for every tile of 32, and is bound by the products,
 // which wait for each tile's loads: two requests of 1000 tokens after 4000 others, 32 / 8 heads
 // of 128, 1387 us, 106 TFLOP/s where an fp32 product of 8192 x 8192 reaches 154.
+// An 8-bit cache has half the bytes, so that the time in which a wave turns codes into bf16 counts:
+// its loads are under way meanwhile, keys and values apart. The 48 requests read 411 MB in 80 us, 5.1
+// TB/s (with both loaded after the products, as above: 106 us for the call, with the keys' loads
+// ahead 83), one token over 131000 keys 270 MB in 46 us, 5.9 TB/s (54.7 and 49.3 for the call). Tiles
+// of 64 keys do not fit in the registers; two tiles of 32 held at once gave 84.2 for 82.9 us.
 template <int WT, int CT, int DH>
 struct AttnTile {
   static constexpr bool kBf = WT == WT_BF16, k8 = CT == CT_E4M3;
@@ -726,7 +731,12 @@ __device__ __forceinline__ void split_attention(const AttendArgs& a, uint32_t bx
 // clocks (the library's product keeps them busy 69%), with no bank conflict in LDS, and the
 // clock falls to 1.6 to 1.9 GHz, as it does for that product, where a kernel bound by memory runs
 // at 2.5. Fewer clocks a key have brought lower clocks: leaving out the whole softmax saves 3%.
-// Heads of 64 have as much softmax for half the products: 370 us, 837 TFLOP/s. The four requests'
+// An 8-bit cache costs the conversion of each stage, once for 128 rows, and its writes to LDS: 650 to
+// 675 us, 915 to 950 TFLOP/s, the matrix cores busy 40% of clocks of 1.9 to 2.0 GHz. One in six of
+// LDS's busy clocks is a conflict of those writes; a layout without any gave 0.5%. The 8-bit matrix
+// product with Q in two e4m3 parts would need no conversion, but its sums are off by up to 2.8e-4 of
+// the products' norm, which is not 32 bits.
+// Heads of 64 have as much softmax for half the products: 370 us, 837 TFLOP/s (8 bits: 409). The four requests'
 // 16-token chunk (82 MB of K and V) reads at 5.8 TB/s between a start of 2 us and the joins.
 typedef __attribute__((ext_vector_type(16))) float f32x16_t;
 typedef __attribute__((ext_vector_type(4))) short i16x4_t;
