@@ -658,8 +658,9 @@ int check_shared(const sfn_kv* kv, int32_t R, int32_t T, int32_t h_q, int32_t ma
   return check_attend(kv, R, T, h_q, max_new, max_shared + max_own);
 }
 
-// A launch's rows of parts in a call over a shared prefix: every row has at least one.
-int64_t shared_parts(int64_t rows, const sfn::AttendPlan& p) { return rows * p.S; }
+// Tokens of a call over a shared prefix that can have parts: every one that is computed has, of
+// both sets of keys.
+int64_t shared_tokens(int32_t R, int32_t T, int32_t max_new) { return std::min<int64_t>(T, (int64_t)R * max_new); }
 
 size_t shared_bytes(const sfn_kv* kv, int64_t own, int64_t prefix) {
   return attend_bytes(kv, own) + attend_bytes(kv, prefix) - sfn::kWsHeader;
@@ -670,7 +671,7 @@ size_t shared_size(const sfn_kv* kv, int32_t R, int32_t T, int32_t h_q, int32_t 
   const int32_t t = T > 0 ? T : 1;
   const int64_t own = sfn::attend_most_parts(R, h_q, kv->h_kv, kv->dtype, max_new, own_span(max_own));
   const int64_t prefix = sfn::prefix_most_parts(t, h_q, kv->h_kv, kv->dtype, max_shared);
-  return shared_bytes(kv, std::max(own, (int64_t)R * max_new * h_q), std::max(prefix, (int64_t)t * h_q));
+  return shared_bytes(kv, std::max(own, shared_tokens(R, t, max_new) * h_q), std::max(prefix, (int64_t)t * h_q));
 }
 
 int attend_shared(const sfn_kv* kv, const uint8_t* k_exp, const uint8_t* v_exp, int32_t R, int32_t T, int32_t h_q, const void* q,
@@ -693,7 +694,7 @@ int attend_shared(const sfn_kv* kv, const uint8_t* k_exp, const uint8_t* v_exp, 
   const sfn::AttendPlan pp = sfn::prefix_plan(T, h_q, kv->h_kv, kv->dtype, max_shared);
   // one launch of 256 threads to a workgroup, whose threads are counted in 32 bits
   if ((int64_t)R * (po.S | 1) * po.row_tiles * kv->h_kv + (int64_t)pp.S * pp.row_tiles * kv->h_kv > UINT32_MAX / 256) return SFN_ESHAPE;
-  const int64_t own_parts = shared_parts((int64_t)R * max_new * h_q, po), prefix_parts = shared_parts((int64_t)T * h_q, pp);
+  const int64_t own_parts = shared_tokens(R, T, max_new) * h_q * po.S, prefix_parts = (int64_t)T * h_q * pp.S;
   if ((st = check_ws(ws, ws_bytes, shared_bytes(kv, own_parts, prefix_parts))) != SFN_OK) return st;
   char* const w = static_cast<char*>(ws) + sfn::kWsHeader;
   sfn::SharedArgs a{};
@@ -702,6 +703,7 @@ int attend_shared(const sfn_kv* kv, const uint8_t* k_exp, const uint8_t* v_exp, 
   a.own.shared = shared_len;
   a.own.max_shared = max_shared;
   a.own.max_own = max_own;
+  a.own.by_token = T < (int64_t)R * max_new;
   a.prefix = a.own;
   set_plan(a.own, po, kv, w, own_parts);
   a.own.table = table;

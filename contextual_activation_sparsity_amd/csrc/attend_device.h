@@ -54,6 +54,12 @@ struct Request {
     past = len - n;
   }
   __device__ __forceinline__ static int shared_len(const AttendArgs& a) { return min(max(gp(a.shared)[0], 0), a.max_shared); }
+  // Where token `tok` of request r has its parts, in tokens: by request, or by token where those
+  // are fewer (calls over a shared prefix, which have parts of every row, split or not).
+  __device__ __forceinline__ int64_t place(const AttendArgs& a, int r, int tok) const {
+    if (KIND == ATTEND_OWN && a.by_token) return t0 + tok;
+    return (int64_t)r * a.max_new + tok;
+  }
 };
 
 // ---- split attention -----------------------------------------------------------------
@@ -693,7 +699,7 @@ __device__ __forceinline__ void split_attention(const AttendArgs& a, uint32_t bx
     if (KIND == ATTEND_PLAIN && a.S == 1) {
       store_row<WT, DH>(a, t0 + tok, head, d4, o, L);
     } else {
-      const int64_t at = (((int64_t)r * a.max_new + tok) * a.h_q + head) * a.S + split;
+      const int64_t at = (req.place(a, r, tok) * a.h_q + head) * a.S + split;
       *reinterpret_cast<SFN_GLOBAL f32x4_t*>(gp(a.part_o) + at * DH + d4) = o;
       if (d4 == 0) {
         float top = s_m[0][x];
@@ -1134,7 +1140,7 @@ __device__ __forceinline__ void tile_attention(const AttendArgs& a, uint32_t bx,
       *reinterpret_cast<f32x4_t*>(out + c * DH * 4 + (((8 * d + 2 * e + h) ^ (c & 15)) * 16)) =
           f32x4_t{w.acc[d][4 * e], w.acc[d][4 * e + 1], w.acc[d][4 * e + 2], w.acc[d][4 * e + 3]} * inv;
   // the lane's row in the output or in the parts, -1 if it has none
-  const int64_t orow = whole ? (int64_t)(t0 + tok) * a.h_q + head : (((int64_t)r * a.max_new + tok) * a.h_q + head) * a.S + split;
+  const int64_t orow = whole ? (int64_t)(t0 + tok) * a.h_q + head : (req.place(a, r, tok) * a.h_q + head) * a.S + split;
   const int own = ok ? (int)orow : -1;
   if (!whole && h == 0 && ok) *reinterpret_cast<SFN_GLOBAL f32x2_t*>(gp(a.part_ml) + 2 * orow) = f32x2_t{w.m, l};
   wave_sync();

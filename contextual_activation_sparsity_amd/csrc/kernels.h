@@ -148,6 +148,7 @@ struct AttendArgs {
   const uint8_t *k_exp, *v_exp;                   // the rows' powers of two of an 8-bit cache, else null
   const int32_t* shared;                          // tokens of the prefix, of a call over a shared one
   int max_shared, max_own;
+  int by_token;                                   // there: the own keys' parts lie by token, else by request and its token
 };  // g = h_q / h_kv, g_mul = ceil(2^21 / g)
 struct AttendPlan {
   int tile_rows, tile_keys;  // query rows of a workgroup, keys it takes at a time

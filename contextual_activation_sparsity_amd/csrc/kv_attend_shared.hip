@@ -78,7 +78,7 @@ __global__ __launch_bounds__(256) void attend_join_shared_kernel(SharedArgs x) {
   const int first = min(max(gp(a.cu)[0], 0), a.T);  // the prefix's parts begin with this token
   const int mine = splits_used(a, req, i, head);
   const int all = mine + (req.past >= shared ? (shared + p.chunk - 1) / p.chunk : 0);
-  const int64_t at_a = (((int64_t)r * a.max_new + i) * a.h_q + head) * a.S;
+  const int64_t at_a = (req.place(a, r, i) * a.h_q + head) * a.S;
   const int token = max(req.t0 + i - first, 0);  // of the prefix's rows; cu that descends stays in them
   const int64_t at_p = ((int64_t)token * a.h_q + head) * p.S;
   const SFN_GLOBAL f32x2_t* ml_a = reinterpret_cast<const SFN_GLOBAL f32x2_t*>(gp(a.part_ml)) + at_a;

@@ -411,12 +411,14 @@ int kv_cache_attend(const sfn_kv* kv, int32_t R, int32_t T, int32_t h_q, const v
  *            request reads from its own row. As there, lengths past them stay in bounds:
  *            *shared_len counts as max_shared (or the tokens of prefix_pages) at most, a kv_len as
  *            *shared_len + max_own at most, or as max_own where the request reads its own row alone.
- *            Offsets cu that do not ascend stay in bounds too; what tokens before cu[0] or behind
- *            cu[R] get is then not defined
+ *            Offsets cu that do not ascend stay in bounds too; what tokens before cu[0], behind
+ *            cu[R] or of two requests get is then not defined
  * Requests with other prefixes are calls of their own (with rows of table, cu and kv_len, as
  * above), and so are prompts beside single tokens: R times the row tiles of max_new tokens are
  * launched, and more than 2^24 of them, over all heads and splits, are refused.
- * Workspace: as kv_cache_attend's, enough for every call with smaller arguments. T = 0 does nothing.
+ * Workspace: as kv_cache_attend's, enough for every call with smaller arguments. Every token has
+ * partial results of both sets of keys, for each of its heads 4 dh + 8 bytes of each, or as often
+ * as its keys are split. T = 0 does nothing.
  */
 size_t kv_cache_attend_shared_workspace_size(const sfn_kv* kv, int32_t R, int32_t T, int32_t h_q, int32_t max_new,
                                              int32_t max_shared, int32_t max_own);
