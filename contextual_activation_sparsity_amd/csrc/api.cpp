@@ -659,8 +659,8 @@ int check_shared(const sfn_kv* kv, int32_t R, int32_t T, int32_t h_q, int32_t ma
 }
 
 // Tokens of a call over a shared prefix that can have parts: every one that is computed has, of
-// both sets of keys.
-int64_t shared_tokens(int32_t R, int32_t T, int32_t max_new) { return std::min<int64_t>(T, (int64_t)R * max_new); }
+// both sets of keys. The step may have others (other calls', or room that a captured step leaves).
+int32_t shared_tokens(int32_t R, int32_t T, int32_t max_new) { return (int32_t)std::min<int64_t>(T, (int64_t)R * max_new); }
 
 size_t shared_bytes(const sfn_kv* kv, int64_t own, int64_t prefix) {
   return attend_bytes(kv, own) + attend_bytes(kv, prefix) - sfn::kWsHeader;
@@ -668,10 +668,10 @@ size_t shared_bytes(const sfn_kv* kv, int64_t own, int64_t prefix) {
 
 size_t shared_size(const sfn_kv* kv, int32_t R, int32_t T, int32_t h_q, int32_t max_new, int32_t max_shared, int32_t max_own) {
   if (check_shared(kv, R, T, h_q, max_new, max_shared, max_own) != SFN_OK) return 0;
-  const int32_t t = T > 0 ? T : 1;
+  const int32_t t = shared_tokens(R, T > 0 ? T : 1, max_new);
   const int64_t own = sfn::attend_most_parts(R, h_q, kv->h_kv, kv->dtype, max_new, own_span(max_own));
   const int64_t prefix = sfn::prefix_most_parts(t, h_q, kv->h_kv, kv->dtype, max_shared);
-  return shared_bytes(kv, std::max(own, shared_tokens(R, t, max_new) * h_q), std::max(prefix, (int64_t)t * h_q));
+  return shared_bytes(kv, std::max(own, (int64_t)t * h_q), std::max(prefix, (int64_t)t * h_q));
 }
 
 int attend_shared(const sfn_kv* kv, const uint8_t* k_exp, const uint8_t* v_exp, int32_t R, int32_t T, int32_t h_q, const void* q,
@@ -691,10 +691,11 @@ int attend_shared(const sfn_kv* kv, const uint8_t* k_exp, const uint8_t* v_exp, 
     if (!aligned4_or_null(p)) return SFN_EALIGN;
   max_new = std::min(max_new, T);
   const sfn::AttendPlan po = sfn::attend_plan(R, h_q, kv->h_kv, kv->dtype, max_new, own_span(max_own), 0);
-  const sfn::AttendPlan pp = sfn::prefix_plan(T, h_q, kv->h_kv, kv->dtype, max_shared);
+  const int32_t tokens = shared_tokens(R, T, max_new);
+  const sfn::AttendPlan pp = sfn::prefix_plan(tokens, h_q, kv->h_kv, kv->dtype, max_shared);
   // one launch of 256 threads to a workgroup, whose threads are counted in 32 bits
   if ((int64_t)R * (po.S | 1) * po.row_tiles * kv->h_kv + (int64_t)pp.S * pp.row_tiles * kv->h_kv > UINT32_MAX / 256) return SFN_ESHAPE;
-  const int64_t own_parts = shared_tokens(R, T, max_new) * h_q * po.S, prefix_parts = (int64_t)T * h_q * pp.S;
+  const int64_t rows = (int64_t)tokens * h_q, own_parts = rows * po.S, prefix_parts = rows * pp.S;
   if ((st = check_ws(ws, ws_bytes, shared_bytes(kv, own_parts, prefix_parts))) != SFN_OK) return st;
   char* const w = static_cast<char*>(ws) + sfn::kWsHeader;
   sfn::SharedArgs a{};
@@ -713,7 +714,8 @@ int attend_shared(const sfn_kv* kv, const uint8_t* k_exp, const uint8_t* v_exp, 
   set_plan(a.prefix, pp, kv, w + (attend_bytes(kv, own_parts) - sfn::kWsHeader), prefix_parts);
   a.prefix.table = prefix;
   a.prefix.max_pages = prefix_pages;
-  a.prefix.max_new = T;
+  a.prefix.max_new = tokens;
+  a.prefix.each_new = max_new;
   a.prefix.max_len = max_shared;
   return hip_status(sfn::launch_kv_attend_shared(a, kv->dh, kv->dtype, static_cast<hipStream_t>(stream)));
 }

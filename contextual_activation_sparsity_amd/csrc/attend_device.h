@@ -30,6 +30,9 @@ enum { ATTEND_PLAIN = 0, ATTEND_PREFIX = 1, ATTEND_OWN = 2 };
 // keys [from, len) are read. The prefix is attended to by all tokens as one request, all of which
 // see every key of it (past = len); the part behind it starts there for a request whose tokens
 // all come after it, and otherwise reads everything from the request's own pages.
+// The prefix's part is made for min(T, R max_new) tokens, `most`. The call's tokens are
+// [cu[0], cu[R]); only where some request has more than max_new can they be more than that, and
+// then the first max_new of each request follow each other there.
 template <int KIND>
 struct Request {
   int t0, n, len, past, from;
@@ -59,6 +62,32 @@ struct Request {
   __device__ __forceinline__ int64_t place(const AttendArgs& a, int r, int tok) const {
     if (KIND == ATTEND_OWN && a.by_token) return t0 + tok;
     return (int64_t)r * a.max_new + tok;
+  }
+  __device__ __forceinline__ static int start(const AttendArgs& a, int r) { return min(max(gp(a.cu)[r], 0), a.T); }
+  // Token `tok` is the step's token first() + tok: for the prefix, whose `most` and whose requests'
+  // bound are max_new and each_new, not the same for all where there are more.
+  __device__ __forceinline__ int first(const AttendArgs& a, int tok) const {
+    if (KIND != ATTEND_PREFIX || n <= a.max_new) return t0;
+    int at = 0, it = -tok;  // where there is none, nothing asks for what it gets
+#pragma unroll 1
+    for (int r = 0; r < a.R; ++r) {  // all of them, so that the loop is the wave's and not the lane's
+      const int from = start(a, r), m = min(max(start(a, r + 1) - from, 0), a.each_new);
+      it = tok >= at && tok < at + m ? from - at : it;
+      at += m;
+    }
+    return it;
+  }
+  // And back, for token i < max_new of request r; one that the prefix's part is not made for
+  // (offsets that descend) is given another.
+  __device__ __forceinline__ int in_prefix(const AttendArgs& a, int most, int r, int i) const {
+    const int c0 = start(a, 0);
+    int at = t0 + i - c0;
+    if (most < a.T && start(a, a.R) - c0 > most) {
+      at = i;
+#pragma unroll 1
+      for (int s = 0; s < r; ++s) at += min(max(start(a, s + 1) - start(a, s), 0), a.max_new);
+    }
+    return min(max(at, 0), most - 1);
   }
 };
 
@@ -543,7 +572,7 @@ __device__ __forceinline__ void split_attention(const AttendArgs& a, uint32_t bx
   for (int x = 0; x < RT; ++x) {
     const bool ok = 16 * x + c <= last;
     const int i = ok ? 16 * x + c : 0, tok = map.token(i), head = hk * g + map.head(i, tok);
-    const SFN_GLOBAL char* src = gp(a.q) + (int64_t)(t0 + tok) * a.q_stride + head * ROW;
+    const SFN_GLOBAL char* src = gp(a.q) + (int64_t)(req.first(a, tok) + tok) * a.q_stride + head * ROW;
 #pragma unroll
     for (int s = 0; s < NQ; ++s) qf[x][s] = ld16(src + C::chunk_at(s, q) * KB);
     row_hi[x] = ok ? min(past + tok + 1, len) : 0;
@@ -1036,7 +1065,7 @@ __device__ __forceinline__ void tile_attention(const AttendArgs& a, uint32_t bx,
   w.m = kNegInf;
   w.l = 0.f;
   {
-    const SFN_GLOBAL char* src = gp(a.q) + (int64_t)(t0 + tok) * a.q_stride + head * ROW + 16 * h;
+    const SFN_GLOBAL char* src = gp(a.q) + (int64_t)(req.first(a, tok) + tok) * a.q_stride + head * ROW + 16 * h;
 #pragma unroll
     for (int s = 0; s < W::NS; ++s) w.q[s] = __builtin_bit_cast(bf16x8_t, ld16(src + 32 * s));
 #pragma unroll

@@ -149,6 +149,7 @@ struct AttendArgs {
   const int32_t* shared;                          // tokens of the prefix, of a call over a shared one
   int max_shared, max_own;
   int by_token;                                   // there: the own keys' parts lie by token, else by request and its token
+  int each_new;                                   // there, for the prefix: the bound on a request's tokens (max_new is on all)
 };  // g = h_q / h_kv, g_mul = ceil(2^21 / g)
 struct AttendPlan {
   int tile_rows, tile_keys;  // query rows of a workgroup, keys it takes at a time
@@ -156,7 +157,7 @@ struct AttendPlan {
   int64_t parts;             // rows of partial results
 };
 AttendPlan attend_plan(int R, int h_q, int h_kv, int dtype, int max_new, int max_len, int window);
-// The part of a call over a shared prefix: T tokens as one request over up to max_shared keys.
+// The part of a call over a shared prefix: T tokens at most, as one request over up to max_shared keys.
 AttendPlan prefix_plan(int T, int h_q, int h_kv, int dtype, int max_shared);
 int64_t prefix_most_parts(int T, int h_q, int h_kv, int dtype, int max_shared);
 // Rows of partial results that no call within these bounds passes.

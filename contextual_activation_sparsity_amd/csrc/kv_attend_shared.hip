@@ -20,7 +20,7 @@ namespace {
 // this takes 9.3, 8 tokens after 2000 shared keys 19.7 (13.2), 48 after 8000 48.2 (46.0), 32 chunks
 // after 60000 665 (641).
 // WAY is how a workgroup takes the rows of one key head: 1 and 2 are split attention with 16 and 32
-// rows, 3 is tile attention. T tokens have at least as many rows as one request's, so the prefix's
+// rows, 3 is tile attention. All tokens have at least as many rows as one request's, so the prefix's
 // way is never the smaller one. The registers of a launch are those of its larger way: with 16 rows
 // in both parts three workgroups share a compute unit, otherwise two.
 // 48 single tokens after 8000 shared keys, each with up to 1200 of its own, 32 / 8 heads of 128,
@@ -75,12 +75,10 @@ __global__ __launch_bounds__(256) void attend_join_shared_kernel(SharedArgs x) {
   const Request<ATTEND_OWN> req(a, r);
   if (i >= req.n) return;
   const int shared = Request<ATTEND_OWN>::shared_len(a);
-  const int first = min(max(gp(a.cu)[0], 0), a.T);  // the prefix's parts begin with this token
   const int mine = splits_used(a, req, i, head);
   const int all = mine + (req.past >= shared ? (shared + p.chunk - 1) / p.chunk : 0);
   const int64_t at_a = (req.place(a, r, i) * a.h_q + head) * a.S;
-  const int token = max(req.t0 + i - first, 0);  // of the prefix's rows; cu that descends stays in them
-  const int64_t at_p = ((int64_t)token * a.h_q + head) * p.S;
+  const int64_t at_p = ((int64_t)req.in_prefix(a, p.max_new, r, i) * a.h_q + head) * p.S;
   const SFN_GLOBAL f32x2_t* ml_a = reinterpret_cast<const SFN_GLOBAL f32x2_t*>(gp(a.part_ml)) + at_a;
   const SFN_GLOBAL f32x2_t* ml_p = reinterpret_cast<const SFN_GLOBAL f32x2_t*>(gp(p.part_ml)) + at_p;
   const int d4 = tid % LD, s0 = tid / LD;

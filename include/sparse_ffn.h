@@ -415,9 +415,10 @@ int kv_cache_attend(const sfn_kv* kv, int32_t R, int32_t T, int32_t h_q, const v
  *            cu[R] or of two requests get is then not defined
  * Requests with other prefixes are calls of their own (with rows of table, cu and kv_len, as
  * above), and so are prompts beside single tokens: R times the row tiles of max_new tokens are
- * launched, and more than 2^24 of them, over all heads and splits, are refused.
- * Workspace: as kv_cache_attend's, enough for every call with smaller arguments. Every token has
- * partial results of both sets of keys, for each of its heads 4 dh + 8 bytes of each, or as often
+ * launched, and more than 2^24 of them, over all heads and splits, are refused. The prefix's share
+ * is divided as if the call had min(T, R max_new) tokens.
+ * Workspace: as kv_cache_attend's, enough for every call with smaller arguments. Each of so many
+ * tokens has partial results of both sets of keys, for each of its heads 4 dh + 8 bytes of each, or as often
  * as its keys are split. T = 0 does nothing.
  */
 size_t kv_cache_attend_shared_workspace_size(const sfn_kv* kv, int32_t R, int32_t T, int32_t h_q, int32_t max_new,

@@ -39,3 +39,25 @@ def test_parts_are_of_the_tokens_and_not_of_the_bounds(R, T, max_new, dtype, e8)
     for r, t, n in {(R, T, max_new), (R, max(1, T // 3), max_new), (max(1, R // 2), T, max_new), (R, T, max(1, max_new // 7)), (1, T, T), (R, T, 1)}:
         if r <= R and n <= max_new:
             assert shared(kv, R=r, T=t, max_new=n, max_shared=prefix, max_own=own, max_pages=9999, prefix_pages=9999, ws=FAKE + 16, ws_bytes=need) == B.SFN_EALIGN
+
+
+@pytest.mark.parametrize("e8", [False, True])
+@pytest.mark.parametrize("dtype", [0, 1])
+@pytest.mark.parametrize("R,max_new", [(4, 1), (3, 16), (1, 1)])
+def test_a_group_of_few_tokens_in_a_large_step(R, max_new, dtype, e8):
+    """Other tokens of the step, of other calls' requests, change nothing about a group's work: the
+    division of the prefix and its parts are those of a step with this group alone."""
+    kv = (_kv8 if e8 else _kv)(dtype=dtype)
+    need = size(kv, R, R * max_new, 32, max_new, 60000, 1000)
+    assert size(kv, R, 2048, 32, max_new, 60000, 1000) == size(kv, R, 262144, 32, max_new, 60000, 1000) == need > 0
+    few = dict(R=R, max_new=max_new, max_shared=60000, max_own=1000, max_pages=9999, prefix_pages=9999)
+
+    # what the call itself asks for
+    def asks(T):
+        lo, hi = HEADER, need
+        while lo < hi:
+            mid = (lo + hi) // 2
+            lo, hi = (lo, mid) if shared(kv, T=T, ws_bytes=mid, ws=FAKE + 16, **few) == B.SFN_EALIGN else (mid + 1, hi)
+        return lo
+
+    assert asks(R * max_new) == asks(2048)

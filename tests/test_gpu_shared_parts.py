@@ -1,9 +1,13 @@
 """Where the parts of attention over a shared prefix lie, against the float64 oracle of each
-request on its own: by request or by token, with tokens that no request has."""
+request on its own: by request or by token, with tokens that no request has, and with bounds that
+are too small."""
 
 import pytest
+import torch
 
-from tests.test_gpu_attend_shared import KINDS, after, check
+from tests.helpers import say
+from tests.serving_helpers import within
+from tests.test_gpu_attend_shared import KINDS, Batch, after, check, tokens
 
 pytestmark = pytest.mark.gpu
 
@@ -23,3 +27,37 @@ def test_parts_by_request_and_by_token(own, pad, dtype, kind):
 @pytest.mark.parametrize("max_new", [10 ** 3, 2 * 10 ** 5])
 def test_bounds_far_above_the_tokens(max_new, dtype, kind):
     check(dtype, kind, 8, 2, 64, 16, 300, after(300, [(30, 3), (2000, 17), (9, 0), (65, 1)]), seed=33, max_new=max_new)
+
+
+@pytest.mark.parametrize("dtype,kind", KINDS)
+@pytest.mark.parametrize("h_q,h_kv", [(8, 2), (16, 1)])
+def test_tokens_past_the_bound_take_no_place_of_others(h_q, h_kv, dtype, kind):
+    """Requests with more tokens than the bound stand before others, which are computed as if the
+    bound were right: in a step with more tokens than the bounds allow, and in one with fewer."""
+    shared = 400
+    for own, max_new in (([(60, 50), (9, 2), (33, 1), (70, 3)], 3), ([(5, 4), (9, 0), (33, 1), (70, 0)], 3), ([(200, 90), (90, 1)], 1),
+                         ([(40, 20), (30, 0), (90, 0), (33, 33), (12, 7)], 8)):
+        say(f"[shared] past the bound {max_new}, {dtype} {kind} {own}")
+        b = Batch(dtype, kind, h_kv, 64, 16, shared, after(shared, own), 34)
+        q = tokens(b, h_q, 64, 34)
+        out = b.run(q, max_new=max_new, pad=11)
+        for sl, want, bound in b.oracle(q):
+            n = min(max_new, sl.stop - sl.start)
+            within(out[sl][:n], want[:n], bound[:n], "computed tokens")
+            assert out[sl][n:].isnan().all()
+
+
+@pytest.mark.parametrize("dtype,kind", KINDS)
+def test_a_group_among_the_tokens_of_a_step(dtype, kind):
+    """Single tokens behind one prompt, with other requests' tokens before and behind them, whose
+    rows of the output stay as they are."""
+    b = Batch(dtype, kind, 2, 128, 16, 3000, after(3000, [(40, 1), (1, 1), (260, 1)]), 35)
+    q = torch.cat([tokens(b, 8, 128, 35 + i)[:n] for i, n in enumerate((3, 3, 3, 2))])
+    alone = tokens(b, 8, 128, 36)
+    q[5:8] = alone
+    b.cu = [5 + c for c in b.cu]
+    out = b.run(q, pad=300)
+    b.cu = [c - 5 for c in b.cu]
+    for sl, want, bound in b.oracle(alone):
+        within(out[5:8][sl], want, bound, f"tokens {sl.start}..{sl.stop}")
+    assert out[:5].isnan().all() and out[8:].isnan().all()
