@@ -888,7 +888,7 @@ struct TileWave {
   // finite were taken out of the stage (see add_not_finite).
   template <class Row>
   __device__ __forceinline__ void step(const SFN_LDS char* stage, int koff, int voff, int kt, bool full, bool odd, float scale_log2,
-                                       Row row, int keys) {
+                                       Row row, int keys, float slack) {
     // the matrix products first: the compute unit's other workgroup then falls out of step and
     // does its softmax meanwhile (614 -> 589 us on the 2048-token prompts)
     __builtin_amdgcn_s_setprio(1);
@@ -920,7 +920,7 @@ struct TileWave {
 #pragma unroll
       for (int i = 0; i < 16; ++i) top = fmaxf(top, s[kb][i]);
     top = swap_pair_max<32>(top) * scale_log2;  // the scale is positive
-    if (__any(top > m + kSlack)) {
+    if (__any(top > m + slack)) {
       const float mn = fmaxf(m, top);
       const float al = mn == kNegInf ? 0.f : exp2_f(m - mn);
       m = mn;
@@ -986,7 +986,8 @@ struct CodeRows {
 // there are half as many parts to write and join as with two workgroups.
 // s_a and s_b are two arrays, so that the compiler knows that the reads of one need not wait for
 // the loads into the other; of each, a group's K stage and its V stage.
-template <int CT, int DH, int KG, int KIND>
+// EXACT: the maximum does not lag (kSlack 0).
+template <int CT, int DH, int KG, int KIND, bool EXACT>
 __device__ __forceinline__ void tile_attention(const AttendArgs& a, uint32_t bx, int split, int r, char (&s_a)[KG * 2 * kTileKeys * DH * 2],
                                                char (&s_b)[KG * 2 * kTileKeys * DH * 2], uint32_t (&s_odd)[4 * KG]) {
   using W = TileWave<CT, DH>;
@@ -1113,7 +1114,7 @@ __device__ __forceinline__ void tile_attention(const AttendArgs& a, uint32_t bx,
     if (kn < k1) load(nxt, rows_in(page, kn));
     if (kt < min(some_hi, k1) && kt + KT > some_lo)
       w.step((SFN_LDS char*)cur, group, group + STAGE, kt, kt >= all_lo && kt + KT <= all_hi, odd, a.scale_log2, v_row,
-             min(KT, len - kt));
+             min(KT, len - kt), EXACT ? 0.f : kSlack);
     if (k8 && kn < k1) put(nxt);
   };
   for (int kr = k0; kr < k1; kr += KG * KT) {

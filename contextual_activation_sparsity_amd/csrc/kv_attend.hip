@@ -18,7 +18,7 @@ __global__ __launch_bounds__(256 * KG, 2) void attend_tile_kernel(AttendArgs a) 
   __shared__ __attribute__((aligned(16))) char s_a[KG * 2 * kTileKeys * DH * 2];
   __shared__ __attribute__((aligned(16))) char s_b[KG * 2 * kTileKeys * DH * 2];
   __shared__ uint32_t s_odd[4 * KG];
-  tile_attention<CT, DH, KG, ATTEND_PLAIN>(a, blockIdx.x, blockIdx.y, blockIdx.z, s_a, s_b, s_odd);
+  tile_attention<CT, DH, KG, ATTEND_PLAIN, false>(a, blockIdx.x, blockIdx.y, blockIdx.z, s_a, s_b, s_odd);
 }
 
 // Joins the splits of one output row (a token's query head): one workgroup for a row, or one

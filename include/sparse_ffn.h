@@ -394,9 +394,9 @@ int kv_cache_attend(const sfn_kv* kv, int32_t R, int32_t T, int32_t h_q, const v
                     size_t ws_bytes, void* stream);
 
 /*
- * Attention of requests whose first tokens are the same (a system prompt, a document): the same
- * results as kv_cache_attend's without a window, but the keys and values of the first
- * *shared_len tokens are read once for all requests of the call, from the pages in `prefix`, and
+ * Attention of requests whose first tokens are the same (a system prompt, a document): what
+ * kv_cache_attend gives without a window, as exactly (sums in another order, so not the same
+ * bits), but the keys and values of the first *shared_len tokens are read once for all requests of the call, from the pages in `prefix`, and
  * those after them from each request's own row of the table. The rows are those of
  * kv_cache_attend: they, and kv_len, count the shared tokens too. Of row entries only those of
  * the pages from token *shared_len on are read, for a request whose new tokens all come after
