@@ -459,8 +459,10 @@ int kv8_cache_append(const sfn_kv8* kv, int32_t T, int32_t h_q, const void* q, i
 
 /*
  * Reads tokens' keys and values back, by slots (as kv_cache_append takes them; any order, a slot
- * as often as wanted): to keep a request's tokens elsewhere, or to append them to another cache
- * (with the same rows of codes, if nothing is rotated again). T <= 262144.
+ * as often as wanted): to keep a request's tokens elsewhere, or to append them to another cache,
+ * where they have the same values if nothing is rotated again. The codes may be others: of a row
+ * whose largest magnitude was rounded down to 1.75 times a power of two the byte is then one lower
+ * and the codes stand for twice as much. T <= 262144.
  *   slot     [T]; a slot outside the cache gives zeros
  *   k_out, v_out  token t's heads at k_out + t * k_stride (elements), each head's dh values
  *            contiguous, in kv.dtype, exact; addresses and strides 16-byte aligned
