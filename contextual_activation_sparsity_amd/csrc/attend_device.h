@@ -943,6 +943,10 @@ struct TileWave {
       }
     l = add[0] + add[1];
     __builtin_amdgcn_s_setprio(1);
+    // The products' code begins at 32 bytes: what other code a launch holds moves it otherwise, and
+    // the 2048-token prompts with it (on one machine 622 or 632 us by its place, 615 here; 16-token chunks
+    // the same). Heads of 64 gain nothing.
+    if constexpr (DH == 128) asm volatile(".p2align 5");
     add_values(stage, voff, pw);
     __builtin_amdgcn_s_setprio(0);
     if (__builtin_expect(odd, 0)) add_not_finite(row, pw, kt, keys);
