@@ -306,9 +306,12 @@ struct KeyTile {
     add_weighted<WT, DH>(v, p, acc, l);
   }
 
-  // Zeroes the values of keys from `keys` on (keys of the tile that the sequence has); returns
-  // whether some other value is not finite, and makes those 0 too.
-  __device__ __forceinline__ bool clean(int keys, int q) {
+  // Zeroes the values of keys from `keys` on (keys of the tile that the sequence has) and, where
+  // OWN, before `from` (places of the prefix's tokens, which may never have been written; with NaN
+  // there 48 tokens after 8016 shared keys took 86 us through weigh()'s long way instead of 44);
+  // returns whether some other value is not finite, and makes those 0 too.
+  template <bool OWN>
+  __device__ __forceinline__ bool clean(int from, int keys, int q) {
     uint32_t top = 0;  // the largest magnitude bits seen: of the bf16 halves, or of the fp32 words
 #pragma unroll
     for (int u = 0; u < C::NG; ++u)
@@ -319,7 +322,7 @@ struct KeyTile {
 #pragma unroll
           for (int w = 0; w < C::VW * C::KB / 4; ++w) {
             uint32_t& x = v[u][j][nb][w];
-            x = 16 * u + j < keys - 4 * q ? x : 0u;
+            x = 16 * u + j < keys - 4 * q && (!OWN || 16 * u + j >= from - 4 * q) ? x : 0u;
             if constexpr (C::kBf) {
               typedef __attribute__((ext_vector_type(2))) uint16_t u16x2_t;
               top = __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2_t, top),
@@ -448,7 +451,8 @@ struct KeyTile<WT, CT_E4M3, DH> {
     }
   }
 
-  __device__ __forceinline__ bool clean(int keys, int q) {
+  template <bool OWN>
+  __device__ __forceinline__ bool clean(int from, int keys, int q) {
     uint32_t odd = 0;
 #pragma unroll
     for (int u = 0; u < C::NG; ++u)
@@ -457,7 +461,7 @@ struct KeyTile<WT, CT_E4M3, DH> {
 #pragma unroll
         for (int w = 0; w < NV; ++w) {
           uint32_t& x = v[u][j][w];
-          x = 16 * u + j < keys - 4 * q ? x : 0u;
+          x = 16 * u + j < keys - 4 * q && (!OWN || 16 * u + j >= from - 4 * q) ? x : 0u;
           odd |= nan_codes(x);
         }
     if (!__any(odd != 0)) return false;
@@ -669,7 +673,7 @@ __device__ __forceinline__ void split_attention(const AttendArgs& a, uint32_t bx
         place(next);
         tile.load_keys(a, row, c, q);
       }
-      const bool odd = full ? false : tile.clean(len - kt, q);
+      const bool odd = full ? false : tile.template clean<KIND == ATTEND_OWN>(req.from - kt, len - kt, q);
 #pragma unroll
       for (int x = 0; x < RT; ++x) weigh(x, s[x], kt, full, odd);
       if (next < k1) {
@@ -677,7 +681,7 @@ __device__ __forceinline__ void split_attention(const AttendArgs& a, uint32_t bx
         if (next + NW * KT < k1) find(next + NW * KT);
       }
     } else {
-      const bool odd = full ? false : tile.clean(len - kt, q);
+      const bool odd = full ? false : tile.template clean<KIND == ATTEND_OWN>(req.from - kt, len - kt, q);
 #pragma unroll
       for (int x = 0; x < RT; ++x) {
         f32x4_t s[NG];
@@ -1092,14 +1096,15 @@ __device__ __forceinline__ void tile_attention(const AttendArgs& a, uint32_t bx,
     // other array is free
     if constexpr (!k8) __builtin_amdgcn_s_waitcnt(kWaitLoads);
     __syncthreads();
-    // A stage with masked keys: what the page holds past the sequence becomes 0, and so do
-    // values that are not finite (0 times one of them is NaN); those count in a way of their own
+    // A stage with masked keys: what the page holds past the sequence, or in places of the
+    // prefix's, becomes 0, and so do values that are not finite (0 times one of them is NaN);
+    // those count in a way of their own
     bool odd = false;
     if (kr + KG * KT > tile_hi || kr < tile_lo) {
       for (int e = kt < k1 ? tid : KT * NC; e < KT * NC; e += 256) {
         uint4* const at = reinterpret_cast<uint4*>(cur + group + STAGE + e * 16);
         const uint4 x = *at;
-        if (kt + e / NC >= len) {
+        if (kt + e / NC >= len || (KIND == ATTEND_OWN && kt + e / NC < req.from)) {
           *at = make_uint4(0, 0, 0, 0);
         } else if (not_finite<WT_BF16>(x.x) | not_finite<WT_BF16>(x.y) | not_finite<WT_BF16>(x.z) | not_finite<WT_BF16>(x.w)) {
           *at = make_uint4(finite_part<WT_BF16>(x.x), finite_part<WT_BF16>(x.y), finite_part<WT_BF16>(x.z), finite_part<WT_BF16>(x.w));

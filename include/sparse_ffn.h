@@ -396,12 +396,13 @@ int kv_cache_attend(const sfn_kv* kv, int32_t R, int32_t T, int32_t h_q, const v
 /*
  * Attention of requests whose first tokens are the same (a system prompt, a document): what
  * kv_cache_attend gives without a window, as exactly (sums in another order, so not the same
- * bits), but the keys and values of the first *shared_len tokens are read once for all requests of the call, from the pages in `prefix`, and
- * those after them from each request's own row of the table. The rows are those of
- * kv_cache_attend: they, and kv_len, count the shared tokens too. Of row entries only those of
- * the pages from token *shared_len on are read, for a request whose new tokens all come after
- * the shared ones (kv_len - n >= *shared_len); a request of which that is not so reads all its
- * keys from its own row. Whole shared pages may simply stand in every row (a plan whose ctx_len
+ * bits), but the keys and values of the first *shared_len tokens are read once for all requests
+ * of the call, from the pages in `prefix`, and those after them from each request's own row of
+ * the table. The rows are those of kv_cache_attend: they, and kv_len, count the shared tokens
+ * too. Of row entries only those of the pages from token *shared_len on count, and of those
+ * pages only the places from that token on, for a request whose new tokens all come after the
+ * shared ones (kv_len - n >= *shared_len); what else a row names may be read, within the cache,
+ * and changes nothing. A request of which that is not so reads all its keys from its own row. Whole shared pages may simply stand in every row (a plan whose ctx_len
  * stays at or above the shared tokens gives none of them back); *shared_len need not be a
  * multiple of the page.
  *   prefix   [prefix_pages]: the pages of the shared tokens, in order (clamped like the table's)

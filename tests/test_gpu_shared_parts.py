@@ -61,3 +61,24 @@ def test_a_group_among_the_tokens_of_a_step(dtype, kind):
     for sl, want, bound in b.oracle(alone):
         within(out[5:8][sl], want, bound, f"tokens {sl.start}..{sl.stop}")
     assert out[:5].isnan().all() and out[8:].isnan().all()
+
+
+@pytest.mark.parametrize("dtype,kind", KINDS)
+@pytest.mark.parametrize("own", [[(60, 1), (1, 1), (900, 1)], [(45, 9), (200, 16)], [(90, 90), (150, 70)]], ids=["one", "chunks", "prompts"])
+@pytest.mark.parametrize("shared,page", [(80, 16), (93, 32), (200, 256), (63, 64)])
+def test_what_a_row_names_before_the_shared_tokens_end_changes_nothing(shared, page, own, dtype, kind):
+    """Entries of the shared tokens' whole pages name the requests' own last pages, and the places of
+    shared tokens in the page that the request goes on in hold NaN."""
+    say(f"[shared] before the prefix's end {shared} page {page} {dtype} {kind} {own}")
+    b = Batch(dtype, kind, 2, 128, page, shared, after(shared, own), 37)
+    q = tokens(b, 8, 128, 37)
+    want = b.run(q)
+    for r in range(len(own)):
+        at = int(b.table[r, shared // page])
+        if kind == "e4m3":
+            for codes, exps in b.cache.parts:
+                codes.view(torch.uint8)[at, :, : shared % page], exps[at, :, : shared % page] = 255, 200
+        else:
+            b.k[at, :, : shared % page], b.v[at, :, : shared % page] = float("inf"), float("nan")
+        b.table[r, : shared // page] = at
+    assert torch.equal(b.run(q), want)
