@@ -2,11 +2,13 @@
 request on its own: by request or by token, with tokens that no request has, and with bounds that
 are too small."""
 
+import numpy as np
 import pytest
 import torch
 
+from oracle import serving as S
 from tests.helpers import say
-from tests.serving_helpers import within
+from tests.serving_helpers import attend_bound, f64, rows_of, within
 from tests.test_gpu_attend_shared import KINDS, Batch, after, check, tokens
 
 pytestmark = pytest.mark.gpu
@@ -82,3 +84,33 @@ def test_what_a_row_names_before_the_shared_tokens_end_changes_nothing(shared, p
             b.k[at, :, : shared % page], b.v[at, :, : shared % page] = float("inf"), float("nan")
         b.table[r, : shared // page] = at
     assert torch.equal(b.run(q), want)
+
+
+@pytest.mark.parametrize("dtype,kind", KINDS)
+@pytest.mark.parametrize("more", [0, 40])
+@pytest.mark.parametrize("h_q,h_kv", [(8, 2), (4, 4)])
+def test_tokens_before_the_first_offset_join_the_prefix_of_its_token(h_q, h_kv, more, dtype, kind):
+    """Offsets that descend name tokens before cu[0], which the prefix's part, of [cu[0], cu[R]), is not
+    made for. What they get is not for use, but it is made of parts that were written: their own
+    keys' and, of the prefix, those of token cu[0]. Any other place would be before the prefix's parts."""
+    shared, n, dh = 700, 2 + more, 64
+    say(f"[shared] offsets that descend, {dtype} {kind} heads={h_q}/{h_kv} n={n}")
+    b = Batch(dtype, kind, h_kv, dh, 16, shared, after(shared, [(20, 0), (30 + n, n), (40 + n, 2 * n)]), 3)
+    b.cu = [2 * n, 0, n, 3 * n]
+    q = tokens(b, h_q, dh, 3)
+    out = b.run(q)
+    first = np.broadcast_to(f64(q[2 * n]), (2 * n, h_q, dh))
+    for r, t0, m in ((1, 0, n), (2, n, n)):
+        past = b.lens[r] - b.news[r]
+        if past < shared:  # of 40 more: it reads its own row alone
+            row, cut = b.table[r], 0
+        else:
+            row, cut = torch.cat([b.prefix[: shared // 16], b.table[r, shared // 16:]]), shared
+        k, v = (f64(rows_of(x, row, b.lens[r])) for x in (b.k, b.v))
+        # queries of two parts, keys that meet one of them: the prefix's the first, the others the second
+        none = np.zeros_like(k)
+        k2 = np.concatenate([np.concatenate([k[:cut], none[:cut]], -1), np.concatenate([none[cut:], k[cut:]], -1)])
+        q2 = np.concatenate([first[t0:t0 + m], f64(q[t0:t0 + m])], -1)
+        want, spread, reach = S.attend(q2, k2, np.concatenate([v, v], -1), np.zeros(m), past + 1 + np.arange(m), dh ** -0.5)
+        bound = attend_bound(want, spread, reach, b.lens[r], dh, dtype)
+        within(out[t0:t0 + m], want[..., :dh], bound[..., :dh], f"tokens {t0}..{t0 + m}")
