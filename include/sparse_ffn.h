@@ -316,6 +316,13 @@ typedef struct sfn_kv {
  *   - its token i has position ctx_len + i and slot table[r][pos / p] * p + pos % p.
  * ctx_len < held_len drops tokens (rejected drafts); ctx_len = new_len = 0 gives back all.
  * The next step's held_len is this step's kv_len.
+ * The plan does not know of pages that stand in several rows (those of a shared prefix, see
+ * kv_cache_attend_shared): dropped from a row they are on the stack, and handed out again, while
+ * other rows use them, once for each row that drops them. So no row of the batch may have a
+ * ctx_len below the tokens of its whole shared pages, S of them. A request that ends or starts over
+ * has ctx_len = S (new_len = 0 to end), and the next in its row held_len = S. Once every request of the
+ * prefix has ended so, one row gives the pages back (held_len = S, ctx_len = new_len = 0), and
+ * the others have held_len = 0 from that plan on.
  *   held_len, ctx_len, new_len  [R]: tokens the pages were taken for, tokens kept of them
  *              (<= held_len), new tokens
  *   table      [R, max_pages]: in, the held pages; out, with the taken pages written;
@@ -402,9 +409,9 @@ int kv_cache_attend(const sfn_kv* kv, int32_t R, int32_t T, int32_t h_q, const v
  * too. Of row entries only those of the pages from token *shared_len on count, and of those
  * pages only the places from that token on, for a request whose new tokens all come after the
  * shared ones (kv_len - n >= *shared_len); what else a row names may be read, within the cache,
- * and changes nothing. A request of which that is not so reads all its keys from its own row. Whole shared pages may simply stand in every row (a plan whose ctx_len
- * stays at or above the shared tokens gives none of them back); *shared_len need not be a
- * multiple of the page.
+ * and changes nothing. A request of which that is not so reads all its keys from its own row.
+ * Whole shared pages may simply stand in every row (kv_cache_plan says how such requests end);
+ * *shared_len need not be a multiple of the page.
  *   prefix   [prefix_pages]: the pages of the shared tokens, in order (clamped like the table's)
  *   shared_len  1 int32, read
  *   max_new  as in kv_cache_attend
