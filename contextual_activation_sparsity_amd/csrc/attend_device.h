@@ -765,17 +765,18 @@ __device__ __forceinline__ void split_attention(const AttendArgs& a, uint32_t bx
 // relative to the result: 0.0021 for the 16-token chunk and 0.0022 for prompts; with kSlack 0
 // 0.0018 and 0.0019, like the split kernel, and 1 to 4% longer for chunks, 6 to 9% for prompts.
 // Two requests of 2048 tokens after 8192 others, 32 / 8 heads of 128: 619 GFLOP in 580 to 625
-// us by the box, 990 to 1065 TFLOP/s, where a sustained bf16 product of 8192 x 8192 reaches
+// us by the machine, 990 to 1065 TFLOP/s, where a sustained bf16 product of 8192 x 8192 reaches
 // 1385. What bounds it is power, and how full the matrix cores are: they are busy half of the
 // clocks (the library's product keeps them busy 69%), with no bank conflict in LDS, and the
 // clock falls to 1.6 to 1.9 GHz, as it does for that product, where a kernel bound by memory runs
 // at 2.5. Fewer clocks a key have brought lower clocks: leaving out the whole softmax saves 3%.
-// An 8-bit cache costs the conversion of each stage, once for 128 rows, and its writes to LDS: 650 to
-// 675 us, 915 to 950 TFLOP/s, the matrix cores busy 40% of clocks of 1.9 to 2.0 GHz. One in six of
+// An 8-bit cache costs the conversion of each stage, once for 128 rows, and its writes to LDS: 655 to
+// 690 us by the machine, 900 to 945 TFLOP/s (up to 730 us where each launch is timed alone), the matrix
+// cores busy 40% of clocks of 1.9 to 2.0 GHz. One in six of
 // LDS's busy clocks is a conflict of those writes; a layout without any gave 0.5%. The 8-bit matrix
 // product with Q in two e4m3 parts would need no conversion, but its sums are off by up to 2.8e-4 of
 // the products' norm, which is not 32 bits.
-// Heads of 64 have as much softmax for half the products: 370 us, 837 TFLOP/s (8 bits: 409). The four requests'
+// Heads of 64 have as much softmax for half the products: 370 us, 837 TFLOP/s (8 bits: 410). The four requests'
 // 16-token chunk (82 MB of K and V) reads at 5.8 TB/s between a start of 2 us and the joins.
 typedef __attribute__((ext_vector_type(16))) float f32x16_t;
 typedef __attribute__((ext_vector_type(4))) short i16x4_t;

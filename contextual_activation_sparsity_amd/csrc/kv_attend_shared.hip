@@ -23,8 +23,8 @@ namespace {
 // rows, 3 is tile attention. All tokens have at least as many rows as one request's, so the prefix's
 // way is never the smaller one. The registers of a launch are those of its larger way: with 16 rows
 // in both parts three workgroups share a compute unit, otherwise two.
-// 48 single tokens after 8000 shared keys, each with up to 1200 of its own, 32 / 8 heads of 128,
-// bf16, 123 MB: 42.5 us, 36 in this launch and 6 to 7 in the join, 2.9 TB/s. The requests' part
+// 48 single tokens after 8000 shared keys, each with up to 1000 of its own, 32 / 8 heads of 128,
+// bf16, 123 MB: 43.2 us, 37 in this launch and 6 to 7 in the join, 2.8 TB/s. The requests' part
 // alone takes 22 us with three workgroups to a compute unit and 31 with two; two tiles of keys held
 // at once there (255 registers), or the first page guessed from the shared length, gave 1 to 2%.
 // The prefix in tiles serves requests whose own keys go through split attention, as all of them
@@ -174,21 +174,22 @@ void launch_shared(SharedArgs a, hipStream_t stream) {
 }  // namespace
 
 // The prefix's keys are the same for all its row tiles, so that their splits can be chosen to fill
-// the chip evenly: of numbers of workgroups up to kHalfRounds quarters of a round (two to a compute
+// the chip evenly: of numbers of workgroups up to kQuarterRounds quarters of a round (two to a compute
 // unit) the one with the lowest cost, which is the stages of the longest chain of rounds, each as
 // long as writing and joining kPartsOfStage rows of parts. 32 chunks of up to 16 tokens after
 // 60000 shared keys, 64 / 8 heads, in 8 bits: 641 us, unsplit (152 workgroups) 1186.
 // kPartsOfStage 3000, with 6500 in brackets, bf16, 32 / 8 heads: 48 single tokens after 8000 shared
 // keys 42.9 us (45.9), 64 after 30000 66.1 (68.9), 4 chunks of 16 after 8000, 64 / 8 heads, 35.4
-// (41.4), 4 prompts of 150 after 4000 47.4 (55.1); with 1500 48 after 8000 in 8 bits 41.3 (37.7).
-constexpr int kSlots = 512, kHalfRounds = 16, kPartsOfStage = 3000;
+// (41.4), 4 prompts of 150 after 4000 47.4 (55.1). With 1500 48 after 8000 in 8 bits take 41.3 us, with
+// 3000 37.7; other shapes were not weighed in 8 bits.
+constexpr int kSlots = 512, kQuarterRounds = 16, kPartsOfStage = 3000;
 AttendPlan prefix_plan(int T, int h_q, int h_kv, int dtype, int max_shared) {
   AttendPlan p = attend_plan(1, h_q, h_kv, dtype, T, max_shared, 0);
   if (p.tile_rows != kTileRows) return p;
   const int64_t base = (int64_t)h_kv * p.row_tiles, span = std::max(1, max_shared), rows = (int64_t)T * h_q;
   auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
   int64_t best = INT64_MAX;
-  for (int k = 0; k <= kHalfRounds; ++k) {
+  for (int k = 0; k <= kQuarterRounds; ++k) {
     const int64_t s = k ? std::min<int64_t>(k * (kSlots / 4) / base, kMaxSplits) : 1;
     if (s < 1) continue;
     const int64_t chunk = up(up(span, s), kTileKeys) * kTileKeys, S = up(span, chunk);
@@ -207,7 +208,7 @@ AttendPlan prefix_plan(int T, int h_q, int h_kv, int dtype, int max_shared) {
 int64_t prefix_most_parts(int T, int h_q, int h_kv, int dtype, int max_shared) {
   const int64_t rows = (int64_t)T * h_q, other = attend_most_parts(1, h_q, h_kv, dtype, T, max_shared);
   const int64_t splits = std::clamp<int64_t>((max_shared + kTileKeys - 1) / kTileKeys, 1, kMaxSplits);
-  return std::max({rows, other, std::min(rows * splits, (int64_t)kTileRows * kHalfRounds * (kSlots / 4))});
+  return std::max({rows, other, std::min(rows * splits, (int64_t)kTileRows * kQuarterRounds * (kSlots / 4))});
 }
 
 hipError_t launch_kv_attend_shared(const SharedArgs& a, int dh, int dtype, hipStream_t stream) {

@@ -31,7 +31,7 @@ namespace {
 // reaches 5.1; with the products in 32 bits it would be 62. Past-the-caches reads, the cache's
 // rows before the queries and 512 threads gave 3 to 8% more time there. Where keys and values
 // are most of it, each wave waits for its rows: 6000 tokens of 16 / 16 heads, 123 MB, 3.4 TB/s.
-// Four tokens 3.0 us, latency.
+// Four tokens 3.0 us in a graph, 3.6 where each launch is timed alone: latency.
 // Four values of a row.
 template <int WT>
 __device__ __forceinline__ void load4(const SFN_GLOBAL char* p, float* f) {
@@ -220,8 +220,8 @@ __global__ __launch_bounds__(256) void kv8_read_kernel(Kv8ReadArgs a) {
 }
 
 // Up to so many tokens, a token's queries and its rows of the cache are a workgroup each, which run
-// side by side (4 tokens, 32 / 8 heads, 3.53 us where one after the other took 4.00); more fill the
-// chip as they are (8000 tokens, 64 / 8 heads, 67 us against 73, 2000 of 32 / 32 20.9 against 20.6).
+// side by side (4 tokens, 32 / 8 heads, when each took half a microsecond more than now, 3.53 us where
+// one after the other took 4.00); more fill the chip as they are (8000 tokens, 64 / 8 heads, 67 us against 73, 2000 of 32 / 32 20.9 against 20.6).
 constexpr int kApart = 1024;
 constexpr int64_t kHeld = 64 << 20;  // bytes that are written past the caches if there are more
 
