@@ -60,8 +60,8 @@ __global__ __launch_bounds__(256, PREFIX_WAY == 1 ? 3 : 2) void attend_shared_ke
   }
 }
 
-// Joins one output row of a call over a shared prefix: the parts of the keys behind it (a, by
-// request) and of the prefix (p, by token), which count where the request's tokens come after it.
+// Joins one output row of a call over a shared prefix: the parts of the keys behind it (a, by request
+// or by token) and of the prefix (p, by token), which count where the request's tokens come after it.
 template <int WT, int DH, bool WAVE>
 __global__ __launch_bounds__(256) void attend_join_shared_kernel(SharedArgs x) {
   const AttendArgs &a = x.own, &p = x.prefix;

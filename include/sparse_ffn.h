@@ -319,10 +319,10 @@ typedef struct sfn_kv {
  * The plan does not know of pages that stand in several rows (those of a shared prefix, see
  * kv_cache_attend_shared): dropped from a row they are on the stack, and handed out again, while
  * other rows use them, once for each row that drops them. So no row of the batch may have a
- * ctx_len below the tokens of its whole shared pages, S of them. A request that ends or starts over
- * has ctx_len = S (new_len = 0 to end), and the next in its row held_len = S. Once every request of the
- * prefix has ended so, one row gives the pages back (held_len = S, ctx_len = new_len = 0), and
- * the others have held_len = 0 from that plan on.
+ * ctx_len below the tokens of its whole shared pages, S of them. A request that ends or starts
+ * over has ctx_len = S (new_len = 0 to end), and the next in its row held_len = S. Once every
+ * request of the prefix has ended so, one row gives the pages back (held_len = S, ctx_len =
+ * new_len = 0), and the others have held_len = 0 from that plan on.
  *   held_len, ctx_len, new_len  [R]: tokens the pages were taken for, tokens kept of them
  *              (<= held_len), new tokens
  *   table      [R, max_pages]: in, the held pages; out, with the taken pages written;
@@ -426,8 +426,8 @@ int kv_cache_attend(const sfn_kv* kv, int32_t R, int32_t T, int32_t h_q, const v
  * launched, and more than 2^24 of them, over all heads and splits, are refused. The prefix's share
  * is divided as if the call had min(T, R max_new) tokens.
  * Workspace: as kv_cache_attend's, enough for every call with smaller arguments. Each of so many
- * tokens has partial results of both sets of keys, for each of its heads 4 dh + 8 bytes of each, or as often
- * as its keys are split. T = 0 does nothing.
+ * tokens has partial results of both sets of keys, 4 dh + 8 bytes of each for each of its heads,
+ * or as often as its keys are split. T = 0 does nothing.
  */
 size_t kv_cache_attend_shared_workspace_size(const sfn_kv* kv, int32_t R, int32_t T, int32_t h_q, int32_t max_new,
                                              int32_t max_shared, int32_t max_own);
